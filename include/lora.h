@@ -575,6 +575,146 @@ int lora_rsvd_write(const lora_store* store_host, int r, const void* A_all, cons
 int lora_rsvd_factor_phases(int n, int d_in, int d_out, int dtype, int r, const void* A_all, const void* B_all,
                             float* sigma, int32_t* status, void* ws, size_t ws_bytes, void* stream, int phases);
 
+/*
+ * 4-bit base layers.  The layers that adapters are added to are often held as
+ * 4-bit codes with a scale (and a zero point) per group of inputs ("Compress
+ * then Serve" section 10 trains its adapters on a 4-bit base).  A w4 store
+ * holds n matrices of one shape, matrix e being
+ *
+ *     W_e[o, k] = s_e[o, g] * (q_e[o, k] - z_e[o, g])      g = k / group
+ *
+ * with q in 0..15, z in 0..15 (8 without zero points) and float32 or bf16
+ * scales: n = 1 for a plain layer, n > 1 for the experts of a layer that is a
+ * mixture of experts.  Codes, scales and zero points are held exactly.
+ *   group       : inputs per scale, a multiple of 32; d_in need not be a
+ *                 multiple of it (the last group is then shorter).
+ *   codes, params : the caller's buffers, laid out by lora_w4_pack.
+ * A plain struct; the caller owns the buffers and keeps them alive.
+ */
+typedef struct lora_w4_store {
+  int32_t n;
+  int32_t d_in;
+  int32_t d_out;
+  int32_t group;
+  int32_t scale_dtype; /* enum lora_dtype */
+  int32_t has_zeros;   /* 0 or 1 */
+  const void* codes;
+  const void* params;
+} lora_w4_store;
+
+/* Most matrices of a store, and most rows (T, or T * k) of a call. */
+#define LORA_W4_MAX_N 1024
+#define LORA_W4_MAX_ROWS (1 << 20)
+
+/*
+ * Size query (host only): bytes of a w4 store's two buffers.  Errors:
+ * INVALID_ARG (null outputs, n < 1, d < 1, group < 1, has_zeros not 0 or 1);
+ * UNSUPPORTED (n above LORA_W4_MAX_N, d_in or d_out not a multiple of 8,
+ * group not a multiple of 32, unknown scale dtype).
+ */
+int lora_w4_bytes(int n, int d_in, int d_out, int group, int scale_dtype, int has_zeros, size_t* code_bytes_host,
+                  size_t* param_bytes_host);
+
+/*
+ * Lay a checkpoint's matrices out.
+ *   q      [n][d_out][d_in / 2]    : codes, two to a byte, input 2 i in the
+ *                                    low four bits of byte i; 4-byte aligned.
+ *   scales [n][d_out][ceil(d_in / group)] : scale_dtype.
+ *   zeros  [n][d_out][ceil(d_in / group)] : bytes 0..15 (the low four bits
+ *                                    are used), or NULL: every zero point 8.
+ *   codes, params : lora_w4_bytes' sizes, 16-byte aligned.
+ *   out_host      : filled on success; the inputs are not referenced.
+ * Errors: as lora_w4_bytes; INVALID_ARG for null pointers; UNSUPPORTED for
+ * misaligned ones.
+ */
+int lora_w4_pack(lora_w4_store* out_host, int n, int d_in, int d_out, int group, const uint8_t* q, const void* scales,
+                 int scale_dtype, const uint8_t* zeros, void* codes, void* params, void* stream);
+
+/*
+ * Workspace of lora_w4_apply (k = 0) and of lora_w4_apply_experts (k >= 1;
+ * weighted: whether weights are given) for T tokens of this dtype (host only;
+ * 0 when none is needed, and on invalid arguments).  Scratch: no
+ * initialization, and not shared by calls in flight together.
+ */
+size_t lora_w4_workspace_bytes(const lora_w4_store* store_host, int dtype, int T, int k, int weighted);
+
+/*
+ * The 4-bit base layer:  y[t] = W x[t]  for a store of one matrix, from one
+ * decode token to a prefill step.  y is overwritten (add the adapters' branch
+ * to it with lora_apply_batched or lora_apply_planned).
+ *   dtype          : of x and y.
+ *   x [T, ldx], y [T, ldy] : rows as in the conventions above; d_in and d_out
+ *                    are multiples of 8 in both dtypes.
+ * q - z is an integer that bf16 holds, so every product is exact in float32;
+ * they are summed in float32 within a group, the groups' sums times their
+ * scales in float32, and y rounds once.  Float32 x is taken in whole (as
+ * three bf16 parts).  Results do not change from call to call.  A row of x
+ * with an infinity or a NaN gives a row of y without finite values; other
+ * rows are not touched by it.  Enqueues one to three kernels.
+ * Errors: INVALID_ARG (null pointers, T < 0, ldx < d_in, ldy < d_out, a store
+ * of several matrices, ws too small); UNSUPPORTED (sizes as lora_w4_bytes,
+ * alignment, T above LORA_W4_MAX_ROWS).
+ */
+int lora_w4_apply(const lora_w4_store* store_host, int dtype, const void* x, int64_t ldx, void* y, int64_t ldy, int T,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The experts' products: each of T tokens takes k of the store's n matrices,
+ * ids [T, k] (as lora_route writes them).
+ *   x_per_choice : 0: x has T rows, every choice of a token reads its row;
+ *                  1: x has T k rows, row t k + j for choice j.
+ *   weights      : NULL: y has T k rows, y[t k + j] = W_{ids[t, j]} x;
+ *                  float32 [T, k]: y has T rows,
+ *                  y[t] = sum_j weights[t, j] W_{ids[t, j]} x, summed in
+ *                  float32 in a fixed order and rounded once.
+ * An id outside [0, n) names no matrix: its row of y is zero, and it adds
+ * nothing to a sum whatever its weight (a token without any gets a row of
+ * zeros); its x row is not read.  The same id may appear twice in a token.
+ * Errors: as lora_w4_apply (a store of several matrices is what it is for);
+ * INVALID_ARG for k < 1 or x_per_choice not 0 or 1; UNSUPPORTED for T k above
+ * LORA_W4_MAX_ROWS.
+ */
+int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void* x, int64_t ldx, int x_per_choice,
+                          void* y, int64_t ldy, int T, int k, const int32_t* ids, const float* weights, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/*
+ * The router: each token's k experts of E, from its logits l[t, :].
+ *   score  : s = softmax(l[t]) over the E experts (LORA_ROUTE_SOFTMAX) or
+ *            s_e = 1 / (1 + exp(-l_e)) (LORA_ROUTE_SIGMOID).
+ *   bias   : float32 [E] or NULL, added to s for the choice alone (a bias
+ *            that balances the experts): c = s + bias, or c = s.
+ *   groups, top_groups : the E experts are `groups` runs of E / groups.  With
+ *            groups > 1 only the top_groups groups of the largest score take
+ *            part: a group's score is its largest c (softmax), or the sum of
+ *            its two largest c (sigmoid; of its one, if it has one).
+ *   ids [T, k]     : out, int32, the k largest c, descending.
+ *   weights [T, k] : out, float32: s of those (without the bias); divided by
+ *            their sum if `renormalize`; then times `scale`.
+ * Ties (of c, and of group scores) go to the lowest index.  An expert whose
+ * logit is NaN or -inf, or whose bias is NaN or -inf, is never chosen (NaN
+ * and -inf logits have s = 0); a logit or bias of +inf counts as the largest
+ * float32.
+ * Where fewer than k experts can be chosen, the rest of the row is id -1 and
+ * weight 0.  A group with fewer than two experts that can be chosen comes
+ * after every other in the sigmoid form (if it has two or more).
+ * Comparisons involving the bias or sums are made in float64, so that the
+ * choice is that of the formula, not of a rounding.
+ *   logits [T, ldl] : dtype rows, ldl >= E, naturally aligned (no 16-byte
+ *            rule).
+ * Errors: INVALID_ARG (null pointers, T < 0, E < 1, k < 1, ldl < E, groups
+ * not a divisor of E, top_groups outside 1..groups, k above the experts of
+ * top_groups groups, an unknown score); UNSUPPORTED (E above
+ * LORA_ROUTE_MAX_EXPERTS, k above LORA_ROUTE_MAX_K, groups above
+ * LORA_ROUTE_MAX_GROUPS, unknown dtype, misaligned pointers).
+ */
+enum lora_route_score { LORA_ROUTE_SOFTMAX = 0, LORA_ROUTE_SIGMOID = 1 };
+#define LORA_ROUTE_MAX_EXPERTS 1024
+#define LORA_ROUTE_MAX_K 32
+#define LORA_ROUTE_MAX_GROUPS 64
+int lora_route(const void* logits, int64_t ldl, int dtype, int T, int E, int k, int score, const float* bias,
+               int groups, int top_groups, int renormalize, float scale, int32_t* ids, float* weights, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,6 +10,13 @@ kernels of librank_specialized.so.  The entry points keep the C names:
     lora_expand(store, h, seg, y)                             # y += s_a B_a h
     lora_apply_batched(store, x, y, ids=ids)                  # all of the above
 
+The 4-bit base layers and the router of a mixture of experts:
+
+    base  = lora_w4_pack(q, scales, zeros, group=128)         # codes of one matrix, or of every expert
+    y     = lora_w4_apply(base, x)                            # y = W x; then lora_apply_batched(store, x, y, ...)
+    ids, w = lora_route(logits, k)                            # a token's experts and their weights
+    y     = lora_w4_apply_experts(experts, x, ids, w)         # y[t] = sum_j w[t, j] W_{ids[t, j]} x
+
 Workspaces (lora_workspace_bytes) are allocated here with torch when the
 caller passes none.
 """
@@ -30,7 +37,8 @@ __all__ = [
     "lora_apply_batched_phases", "lora_apply_batched_noalloc", "lora_apply_launches", "lora_apply_base_fused", "JDStore", "lora_jd_pack", "lora_jd_workspace_bytes",
     "lora_jd_apply", "lora_ranks_uniform", "lora_ranks_spectral", "RsvdFactors", "lora_rsvd_workspace_bytes",
     "lora_rsvd_factor", "lora_rsvd_write", "MultiStore", "lora_pack_multi", "lora_multi_workspace_bytes",
-    "lora_apply_multi", "load_library",
+    "lora_apply_multi", "W4Store", "lora_w4_bytes", "lora_w4_pack", "lora_w4_workspace_bytes", "lora_w4_apply",
+    "lora_w4_apply_experts", "lora_route", "load_library",
 ]
 
 _DTYPES = {torch.bfloat16: L.LORA_DTYPE_BF16, torch.float32: L.LORA_DTYPE_F32}
@@ -590,3 +598,204 @@ def lora_apply_multi(store: MultiStore, x: torch.Tensor, ys: Sequence[torch.Tens
         store.ref(), _p(x), _rows(x, "x"), yp, ld, T, _p(ids), _p(so), _p(pm), ws.data_ptr(), ws.numel(),
         _stream(x)))
     return ys
+
+
+@dataclass
+class W4Store:
+    """4-bit matrices laid out by lora_w4_pack: the C struct plus its buffers."""
+
+    c: L.lora_w4_store
+    codes: torch.Tensor
+    params: torch.Tensor
+
+    @property
+    def n(self) -> int:
+        return self.c.n
+
+    @property
+    def d_in(self) -> int:
+        return self.c.d_in
+
+    @property
+    def d_out(self) -> int:
+        return self.c.d_out
+
+    @property
+    def group(self) -> int:
+        return self.c.group
+
+    def ref(self):
+        return C.byref(self.c)
+
+    def clone(self) -> "W4Store":
+        """An independent copy in fresh device memory (same layout)."""
+        codes, params = self.codes.clone(), self.params.clone()
+        c = L.lora_w4_store.from_buffer_copy(self.c)
+        c.codes, c.params = codes.data_ptr(), params.data_ptr()
+        return W4Store(c, codes, params)
+
+
+def _on(device: torch.device, **tensors) -> None:
+    """Every tensor given is on `device`, a GPU."""
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a GPU")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _ld(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D tensor; of at most one row, its length (its stride is then any number)."""
+    if t.dim() != 2 or t.shape[0] > 1 or (t.shape[0] == 1 and t.shape[1] > 1 and t.stride(1) != 1):
+        return _rows(t, name)
+    return t.shape[1]
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be bfloat16 or float32")
+    return _DTYPES[t.dtype]
+
+
+def lora_w4_bytes(n: int, d_in: int, d_out: int, group: int, scale_dtype: torch.dtype, has_zeros: bool):
+    """Bytes of a w4 store's codes and params buffers."""
+    a, b = C.c_size_t(), C.c_size_t()
+    L.check("lora_w4_bytes", L.lib().lora_w4_bytes(n, d_in, d_out, group, _DTYPES[scale_dtype], int(has_zeros),
+                                                   C.byref(a), C.byref(b)))
+    return a.value, b.value
+
+
+def lora_w4_pack(q: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None, *,
+                 group: int) -> W4Store:
+    """Lay 4-bit matrices out: W[o, k] = scales[o, k // group] * (q[o, k] - zeros[o, k // group]).
+
+    q: uint8 [n, d_out, d_in / 2] (or [d_out, d_in / 2] for one matrix), input
+    2 i in the low four bits of byte i; scales (bfloat16 or float32) and zeros
+    (uint8 0..15; None: 8) [n, d_out, ceil(d_in / group)]."""
+    if q.dim() == 2:
+        q, scales = q.unsqueeze(0), scales.unsqueeze(0)
+        zeros = zeros.unsqueeze(0) if zeros is not None else None
+    if q.dim() != 3 or q.dtype != torch.uint8:
+        raise ValueError("q must be uint8 [n, d_out, d_in / 2]")
+    n, d_out, half = q.shape
+    d_in = 2 * half
+    group = int(group)
+    if group < 1:
+        raise ValueError("group must be positive")
+    shape = (n, d_out, -(-d_in // group))
+    if scales.shape != shape:
+        raise ValueError(f"scales must be {shape}")
+    if zeros is not None and (zeros.shape != shape or zeros.dtype != torch.uint8):
+        raise ValueError(f"zeros must be uint8 {shape}")
+    sd = _dtype(scales, "scales")
+    _on(q.device, scales=scales, zeros=zeros)
+    q, scales = q.contiguous(), scales.contiguous()
+    zeros = zeros.contiguous() if zeros is not None else None
+    cb, pb = lora_w4_bytes(n, d_in, d_out, group, scales.dtype, zeros is not None)
+    codes = torch.empty(cb, dtype=torch.uint8, device=q.device)
+    params = torch.empty(pb, dtype=torch.uint8, device=q.device)
+    c = L.lora_w4_store()
+    with torch.cuda.device(q.device):
+        L.check("lora_w4_pack", L.lib().lora_w4_pack(C.byref(c), n, d_in, d_out, group, _p(q), _p(scales), sd,
+                                                     _p(zeros), codes.data_ptr(), params.data_ptr(), _stream(q)))
+    return W4Store(c, codes, params)
+
+
+def lora_w4_workspace_bytes(store: W4Store, dtype: torch.dtype, T: int, k: int = 0, weighted: bool = False) -> int:
+    """Workspace of lora_w4_apply (k = 0) or lora_w4_apply_experts for T tokens."""
+    return int(L.lib().lora_w4_workspace_bytes(store.ref(), _DTYPES[dtype], int(T), int(k), int(weighted)))
+
+
+def _w4_out(y, rows: int, store: W4Store, x: torch.Tensor) -> torch.Tensor:
+    if y is None:
+        return torch.empty(rows, store.d_out, dtype=x.dtype, device=x.device)
+    if y.shape != (rows, store.d_out) or y.dtype != x.dtype:
+        raise ValueError(f"y must be [{rows}, {store.d_out}] of x's dtype")
+    return y
+
+
+def _w4_ws(store: W4Store, x: torch.Tensor, T: int, k: int, weighted: bool, ws):
+    if ws is None:
+        nb = lora_w4_workspace_bytes(store, x.dtype, T, k, weighted)
+        ws = torch.empty(nb, dtype=torch.uint8, device=x.device) if nb else None
+    return ws
+
+
+def lora_w4_apply(store: W4Store, x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                  ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[t] = W x[t] (overwrites y; allocated when None): the 4-bit base layer
+    of a store of one matrix, x [T, d_in] bfloat16 or float32."""
+    dt, ldx = _dtype(x, "x"), _ld(x, "x")
+    if x.shape[1] != store.d_in:
+        raise ValueError("x must be [T, d_in]")
+    T = x.shape[0]
+    y = _w4_out(y, T, store, x)
+    _on(store.codes.device, x=x, y=y, ws=ws)
+    ws = _w4_ws(store, x, T, 0, False, ws)
+    with torch.cuda.device(x.device):
+        L.check("lora_w4_apply", L.lib().lora_w4_apply(
+            store.ref(), dt, _p(x), ldx, _p(y), _ld(y, "y"), T, _p(ws), ws.numel() if ws is not None else 0, _stream(x)))
+    return y
+
+
+def lora_w4_apply_experts(store: W4Store, x: torch.Tensor, ids: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                          y: Optional[torch.Tensor] = None, *, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The products with the experts that ids [T, k] (int32) name; an id
+    outside [0, n) names none.
+
+    x: [T, d_in] (every choice of a token reads its row) or [T k, d_in].
+    Without weights y is [T k, d_out], a row per choice (zero without an
+    expert); with weights (float32 [T, k]) y is [T, d_out], the weighted sum
+    over a token's choices."""
+    if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 [T, k]")
+    T, k = ids.shape
+    dt, ldx = _dtype(x, "x"), _ld(x, "x")
+    if x.shape[1] != store.d_in or x.shape[0] not in (T, T * k):
+        raise ValueError("x must be [T, d_in] or [T k, d_in]")
+    if weights is not None and (weights.shape != (T, k) or weights.dtype != torch.float32
+                                or not weights.is_contiguous()):
+        raise ValueError("weights must be a contiguous float32 [T, k]")
+    y = _w4_out(y, T if weights is not None else T * k, store, x)
+    _on(store.codes.device, x=x, ids=ids, weights=weights, y=y, ws=ws)
+    ws = _w4_ws(store, x, T, k, weights is not None, ws)
+    with torch.cuda.device(x.device):
+        L.check("lora_w4_apply_experts", L.lib().lora_w4_apply_experts(
+            store.ref(), dt, _p(x), ldx, int(x.shape[0] != T), _p(y), _ld(y, "y"), T, k, _p(ids), _p(weights),
+            _p(ws), ws.numel() if ws is not None else 0, _stream(x)))
+    return y
+
+
+_SCORES = {"softmax": L.LORA_ROUTE_SOFTMAX, "sigmoid": L.LORA_ROUTE_SIGMOID}
+
+
+def lora_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+               groups: int = 1, top_groups: int = 1, renormalize: bool = True, scale: float = 1.0,
+               ids: Optional[torch.Tensor] = None, weights: Optional[torch.Tensor] = None):
+    """The router: (ids int32 [T, k], weights float32 [T, k]) of each token's k
+    experts, by descending score (softmax or sigmoid of logits [T, E], plus
+    bias [E] for the choice alone), among the best top_groups of `groups`
+    runs of experts.  Where fewer than k can be chosen: id -1, weight 0."""
+    dt, ldl = _dtype(logits, "logits"), _ld(logits, "logits")
+    T, E = logits.shape
+    if score not in _SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if bias is not None and (bias.shape != (E,) or bias.dtype != torch.float32 or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous float32 [E]")
+    k = int(k)
+    if k < 1:
+        raise ValueError("k must be positive")
+    if ids is None:
+        ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+    if ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 [T, k]")
+    if weights.shape != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 [T, k]")
+    _on(logits.device, bias=bias, ids=ids, weights=weights)
+    with torch.cuda.device(logits.device):
+        L.check("lora_route", L.lib().lora_route(
+            _p(logits), ldl, dt, T, E, k, _SCORES[score], _p(bias), int(groups), int(top_groups), int(renormalize),
+            float(scale), _p(ids), _p(weights), _stream(logits)))
+    return ids, weights

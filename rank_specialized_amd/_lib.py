@@ -49,6 +49,21 @@ class lora_multi_store(C.Structure):
     ]
 
 
+class lora_w4_store(C.Structure):
+    _fields_ = [
+        ("n", C.c_int32), ("d_in", C.c_int32), ("d_out", C.c_int32), ("group", C.c_int32),
+        ("scale_dtype", C.c_int32), ("has_zeros", C.c_int32), ("codes", C.c_void_p), ("params", C.c_void_p),
+    ]
+
+
+LORA_W4_MAX_N = 1024
+LORA_W4_MAX_ROWS = 1 << 20
+LORA_ROUTE_SOFTMAX = 0
+LORA_ROUTE_SIGMOID = 1
+LORA_ROUTE_MAX_EXPERTS = 1024
+LORA_ROUTE_MAX_K = 32
+LORA_ROUTE_MAX_GROUPS = 64
+
 # name -> (restype, argtypes); mirrors include/lora.h
 P = C.c_void_p
 I = C.c_int
@@ -86,6 +101,12 @@ SIGNATURES = {
     "lora_multi_workspace_bytes": (SZ, [C.POINTER(lora_multi_store), I]),
     "lora_apply_multi": (I, [C.POINTER(lora_multi_store), P, I64, P, P, I, P, P, P, P, SZ, P]),
     "lora_apply_multi_planned": (I, [C.POINTER(lora_multi_store), P, I64, P, P, I, P, SZ, P, SZ, P]),
+    "lora_w4_bytes": (I, [I, I, I, I, I, I, C.POINTER(SZ), C.POINTER(SZ)]),
+    "lora_w4_pack": (I, [C.POINTER(lora_w4_store), I, I, I, I, P, P, I, P, P, P, P]),
+    "lora_w4_workspace_bytes": (SZ, [C.POINTER(lora_w4_store), I, I, I, I]),
+    "lora_w4_apply": (I, [C.POINTER(lora_w4_store), I, P, I64, P, I64, I, P, SZ, P]),
+    "lora_w4_apply_experts": (I, [C.POINTER(lora_w4_store), I, P, I64, I, P, I64, I, I, P, P, P, SZ, P]),
+    "lora_route": (I, [P, I64, I, I, I, I, I, P, I, I, I, C.c_float, P, P, P]),
 }
 
 _lib = None

@@ -12,7 +12,7 @@
 
 namespace lora {
 static thread_local int g_last_hip = 0;
-static int hip_fail(hipError_t e) {
+int hip_fail(hipError_t e) {
   g_last_hip = (int)e;
   return LORA_ERR_HIP;
 }

@@ -13,6 +13,9 @@ namespace lora {
 
 constexpr int kMaxDevices = 64;
 
+// Records `e` for lora_last_hip_error and returns LORA_ERR_HIP.
+int hip_fail(hipError_t e);
+
 // The calling thread's current device, checked against the caches' size.
 inline hipError_t current_device(int* dev) {
   hipError_t e = hipGetDevice(dev);

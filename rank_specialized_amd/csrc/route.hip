@@ -1,0 +1,266 @@
+// The router: each token's k experts of E and their weights
+// (lora_route in include/lora.h).
+//
+// One wave per token, expert e on lane e % 64, value e / 64, so that a row's
+// logits are one coalesced load per 64 experts and stay in registers.  The
+// choice runs on integer keys that order as the numbers do (0: cannot be
+// chosen): without a bias, c orders as the logits themselves do, in both
+// scores, so the keys are the float32 logits and no score is computed for the
+// choice; with a bias, or where two scores are added (the sigmoid form's
+// groups), c is formed in float64, whose rounding is far below the distance
+// of different scores, so that the choice is the formula's.  Each of the k
+// steps takes the wave's largest key (four lane exchanges and a scalar
+// maximum of the four rows) and its lowest index, and drops it; weights are
+// computed at the end, by the k lanes that hold the chosen logits.
+#include <float.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "device_common.h"
+#include "w4_kernels.h"
+
+namespace lora {
+namespace {
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  const auto mx = [](uint32_t a, int b) { return a > (uint32_t)b ? a : (uint32_t)b; };
+  v = mx(v, __builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));   // quad_perm 1,0,3,2
+  v = mx(v, __builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));   // quad_perm 2,3,0,1
+  v = mx(v, __builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
+  v = mx(v, __builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));  // row_mirror
+  uint32_t r = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) r = mx(r, __builtin_amdgcn_readlane((int)v, 16 * i));
+  return r;
+}
+
+// Keys: unsigned integers in the order of the numbers, 0 below every number.
+struct Key32 {
+  uint32_t v;
+  __device__ static Key32 none() { return {0u}; }
+  __device__ static Key32 of(double) = delete;
+  __device__ static Key32 of(float f) {
+    const uint32_t u = __float_as_uint(f + 0.f);  // -0 as 0
+    return {(u & 0x80000000u) ? ~u : u | 0x80000000u};
+  }
+  __device__ bool any() const { return v != 0u; }
+  __device__ bool above(Key32 o) const { return v > o.v; }
+  __device__ bool same(Key32 o) const { return v == o.v; }
+  __device__ static Key32 wave_largest(Key32 k) { return {wave_max(k.v)}; }
+};
+struct Key64 {
+  uint64_t v;
+  __device__ static Key64 none() { return {0ull}; }
+  __device__ static Key64 of(double f) {
+    const uint64_t u = (uint64_t)__double_as_longlong(f + 0.0);
+    return {(u >> 63) ? ~u : u | (1ull << 63)};
+  }
+  __device__ bool any() const { return v != 0ull; }
+  __device__ bool above(Key64 o) const { return v > o.v; }
+  __device__ bool same(Key64 o) const { return v == o.v; }
+  __device__ static Key64 wave_largest(Key64 k) {
+    const uint32_t hi = wave_max((uint32_t)(k.v >> 32));
+    const uint32_t lo = wave_max((uint32_t)(k.v >> 32) == hi ? (uint32_t)k.v : 0u);
+    return {((uint64_t)hi << 32) | lo};
+  }
+  __device__ double value() const {
+    const uint64_t u = (v >> 63) ? v & ~(1ull << 63) : ~v;
+    return __longlong_as_double((long long)u);
+  }
+};
+
+__device__ __forceinline__ float wave_max_f(float v) {  // of numbers and -inf
+  const uint32_t k = wave_max(Key32::of(v).v);
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+template <typename E>
+__device__ __forceinline__ float logit_at(const void* p, int64_t i) {
+  if constexpr (E::kBytes == 2) return bf16_lo(reinterpret_cast<const uint16_t*>(p)[i]);
+  else return reinterpret_cast<const float*>(p)[i];
+}
+
+// WIDE: keys are the float64 c; else the logits.
+template <typename E, int NV, bool WIDE>
+__global__ __launch_bounds__(256) void route_kernel(const RouteArgs p) {
+  typedef typename std::conditional<WIDE, Key64, Key32>::type Key;
+  const int lane = (int)threadIdx.x & 63;
+  const int t = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6);
+  if (t >= p.T) return;
+  const int64_t row = (int64_t)t * p.ldl;
+  constexpr float kNone = -INFINITY;
+  float l[NV];  // logits; -inf: none (past E, NaN)
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = 64 * i + lane;
+    const float v = e < p.E ? logit_at<E>(p.logits, row + e) : kNone;
+    l[i] = v == v ? fminf(v, FLT_MAX) : kNone;
+  }
+  const bool softmax = p.score == LORA_ROUTE_SOFTMAX;
+  // The softmax's maximum and sum over all experts, where the scores
+  // themselves are needed (c with a bias; weights that keep their sum).
+  float top = 0.f;
+  double sum = 1.0;
+  if (softmax && (WIDE || !p.renormalize)) {
+    float m = kNone;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, l[i]);
+    top = wave_max_f(m);
+    if (top == kNone) top = 0.f;
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s += l[i] == kNone ? 0.0 : (WIDE ? exp((double)l[i] - (double)top) : (double)expf(l[i] - top));
+    sum = wave_sum_f64(s);
+  }
+
+  Key key[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    key[i] = Key::none();
+    if (l[i] == kNone) continue;
+    if constexpr (WIDE) {
+      double c = softmax ? exp((double)l[i] - (double)top) / sum : 1.0 / (1.0 + exp(-(double)l[i]));
+      if (p.bias) {
+        const float b = p.bias[64 * i + lane];
+        c += b > FLT_MAX ? (double)FLT_MAX : (double)b;  // a NaN stays one
+      }
+      if (c == c && c != -INFINITY) key[i] = Key::of(c);
+    } else {
+      key[i] = Key::of(l[i]);
+    }
+  }
+
+  if (p.groups > 1) {
+    // Group g's score on lane g (groups <= 64): its largest key, or the sum
+    // of its two largest c.
+    const int n = p.E / p.groups;
+    Key mine = Key::none();
+    for (int g = 0; g < p.groups; ++g) {
+      Key a = Key::none(), b = Key::none();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = 64 * i + lane;
+        if (e >= g * n && e < (g + 1) * n) {
+          if (key[i].above(a)) {
+            b = a;
+            a = key[i];
+          } else if (key[i].above(b)) {
+            b = key[i];
+          }
+        }
+      }
+      Key score = Key::wave_largest(a);
+      if constexpr (WIDE) {
+        if (!softmax && n > 1) {
+          // The second largest: the largest is taken out on one lane.
+          const uint64_t at = __ballot(a.same(score));
+          const Key rest = Key::wave_largest(lane == __ffsll((unsigned long long)at) - 1 ? b : a);
+          score = score.any() && rest.any() ? Key::of(score.value() + rest.value()) : Key::none();
+        }
+      }
+      if (lane == g) mine = score;
+    }
+    // A group's rank: those with a larger score, or the same and a lower index.
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      Key o;
+      if constexpr (WIDE) {
+        o.v = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine.v >> 32), g) << 32) |
+              (uint32_t)__builtin_amdgcn_readlane((int)mine.v, g);
+      } else {
+        o.v = (uint32_t)__builtin_amdgcn_readlane((int)mine.v, g);
+      }
+      rank += o.above(mine) || (o.same(mine) && g < lane) ? 1 : 0;
+    }
+    const uint64_t keep = __ballot(lane < p.groups && rank < p.top_groups);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int g = (64 * i + lane) / n;
+      if (g >= p.groups || !((keep >> g) & 1)) key[i] = Key::none();
+    }
+  }
+
+  // ---- the k largest, descending; lane j keeps the j-th
+  int id = -1;
+  float chosen = kNone;
+  for (int j = 0; j < p.k; ++j) {
+    Key best = key[0];
+    int bi = 0;
+#pragma unroll
+    for (int i = 1; i < NV; ++i)
+      if (key[i].above(best)) {
+        best = key[i];
+        bi = i;
+      }
+    const Key m = Key::wave_largest(best);
+    if (!m.any()) break;  // no expert left (the same in every lane)
+    const uint64_t at = __ballot(best.same(m));
+    int win = __ffsll((unsigned long long)at) - 1;
+    if (__popcll(at) > 1) {  // equal: the lowest index, value first
+      const uint32_t far = best.same(m) ? (uint32_t)(64 * bi + lane) : 0xffffffffu;
+      win = (int)(~wave_max(~far) & 63u);
+    }
+    float bl = l[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) bl = bi == i ? l[i] : bl;
+    const int we = __builtin_amdgcn_readlane(64 * bi + lane, win);
+    const float wl = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bl), win));
+    if (lane == j) {
+      id = we;
+      chosen = wl;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (64 * i + lane == we) key[i] = Key::none();
+  }
+
+  // ---- weights.  Renormalized ones are formed relative to the largest
+  // chosen score, so that small scores do not vanish before the division.
+  const bool have = id >= 0;
+  double w = 0.0;
+  if (softmax) {
+    const float ref = p.renormalize ? wave_max_f(chosen) : top;
+    if (have) w = WIDE ? exp((double)chosen - (double)ref) : (double)expf(chosen - ref);
+    if (!p.renormalize) w /= sum;
+  } else {
+    const double ref = p.renormalize ? fmin((double)wave_max_f(chosen), 0.0) : 0.0;
+    const double c = (double)chosen;
+    if (have) w = c > 0.0 ? 1.0 / (1.0 + exp(-c)) : exp(c - ref) / (1.0 + exp(c));
+  }
+  if (p.renormalize) {
+    const double s = wave_sum_f64(w);
+    w = have ? w / s : 0.0;
+  }
+  if (lane < p.k) {
+    const int64_t at = (int64_t)t * p.k + lane;
+    p.ids[at] = id;
+    p.weights[at] = (float)(w * (double)p.scale);
+  }
+}
+
+template <typename E, bool WIDE>
+hipError_t launch_sized(const RouteArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.T + 3) / 4)), block(256);
+  if (a.E <= 64) hipLaunchKernelGGL((route_kernel<E, 1, WIDE>), grid, block, 0, stream, a);
+  else if (a.E <= 128) hipLaunchKernelGGL((route_kernel<E, 2, WIDE>), grid, block, 0, stream, a);
+  else if (a.E <= 256) hipLaunchKernelGGL((route_kernel<E, 4, WIDE>), grid, block, 0, stream, a);
+  else if (a.E <= 512) hipLaunchKernelGGL((route_kernel<E, 8, WIDE>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((route_kernel<E, 16, WIDE>), grid, block, 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t stream) {
+  const bool wide = a.bias != nullptr || (a.groups > 1 && a.score == LORA_ROUTE_SIGMOID);
+  if (dtype == LORA_DTYPE_BF16) return wide ? launch_sized<BF16, true>(a, stream) : launch_sized<BF16, false>(a, stream);
+  return wide ? launch_sized<F32, true>(a, stream) : launch_sized<F32, false>(a, stream);
+}
+
+}  // namespace lora

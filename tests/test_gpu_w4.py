@@ -1,0 +1,378 @@
+"""The 4-bit base products on the GPU against the float64 oracle.
+
+Tolerance of a value.  Every product (16 + q) x or (q - z) x is exact in
+float32 (a bf16 value, or a bf16 part of a float32 one, times an integer below
+32).  A product then passes through at most `gran` + 2 additions inside its
+group of `gran` <= 128 inputs, one scaling, and the additions of the groups
+and of the waves: gran + groups + 32 roundings in all, each at most 2^-23 of
+the magnitudes added up (a matrix core may truncate).  Those are bounded by
+sum |s| (16 + q + 16 + z) |x| (the products and the correction, in absolute
+value).  A weighted sum multiplies each of its rows' bounds by the weight and
+adds k + 2 roundings.  y then rounds once: half a step, 2^-8 (bf16) or 2^-24
+(float32) of the value.  The f16 form holds x to 2^-25 of its row's largest
+value: x of below 2^-14 of that is rounded by at most 2^-39 of it; d_in of
+those, at |s| 15 each, are inside the same bound (2^-23 of the largest alone).
+"""
+import numpy as np
+import pytest
+import torch
+
+import rank_specialized_amd as rs
+from gpu_helpers import device, hbits, note
+from oracle.w4_ref import experts_ref, w4_apply_ref, w4_magnitude_ref
+from workloads import round_to_bf16
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def make(seed, n, d_out, d_in, group, zeros, scales):
+    rng = np.random.default_rng(seed)
+    packed = rng.integers(0, 256, (n, d_out, d_in // 2), dtype=np.uint8)
+    shape = (n, d_out, -(-d_in // group))
+    s = np.exp(0.3 * rng.normal(size=shape)) / (4.6 * np.sqrt(d_in))
+    s = round_to_bf16(s.astype(np.float32)) if scales == "bf16" else s.astype(np.float32)
+    z = rng.integers(0, 16, shape).astype(np.uint8) if zeros else None
+    return packed, np.asarray(s, np.float32), z
+
+
+def pack(packed, s, z, group, scales, dev):
+    return rs.lora_w4_pack(torch.from_numpy(packed).to(dev), torch.from_numpy(s).to(dev).to(DT[scales]),
+                           None if z is None else torch.from_numpy(z).to(dev), group=group)
+
+
+def acts(seed, rows, d, dtype):
+    x = np.random.default_rng(seed).normal(size=(rows, d)).astype(np.float32)
+    return round_to_bf16(x) if dtype == "bf16" else x
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def tolerance(ref, mag, d_in, group, dtype, k=0):
+    gran = min(128, group)
+    steps = gran + -(-d_in // gran) + 32 + (k + 2 if k else 0)
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    return half * np.abs(ref) * (1 + 2.0 ** -8) + steps * 2.0 ** -23 * mag + 1e-30
+
+
+def assert_close(y, ref, mag, *a, **kw):
+    err, tol = np.abs(host(y) - ref), tolerance(ref, mag, *a, **kw)
+    worst = float((err / tol).max()) if err.size else 0.0
+    assert np.isfinite(host(y)).all() and worst <= 1.0, f"{worst:.3g} of the tolerance"
+
+
+# T, d_in, d_out, group, zeros, scales, dtype
+DENSE = [
+    (1, 128, 16, 128, False, "bf16", "bf16"),
+    (1, 8, 8, 32, False, "bf16", "bf16"),
+    (1, 136, 24, 64, True, "bf16", "bf16"),
+    (1, 3584, 512, 128, False, "bf16", "bf16"),
+    (2, 264, 40, 32, True, "f32", "bf16"),
+    (3, 1000, 72, 96, True, "bf16", "bf16"),
+    (15, 1032, 200, 128, False, "f32", "bf16"),
+    (16, 512, 128, 64, False, "bf16", "bf16"),
+    (17, 520, 136, 64, True, "bf16", "bf16"),
+    (33, 768, 264, 256, True, "bf16", "bf16"),
+    (70, 2056, 248, 32, False, "bf16", "bf16"),
+    (127, 384, 520, 128, True, "bf16", "bf16"),
+    (200, 1152, 1032, 128, False, "bf16", "bf16"),
+    (513, 776, 328, 64, True, "bf16", "bf16"),
+    (1030, 512, 776, 32, True, "f32", "bf16"),
+    (2049, 264, 1096, 128, False, "bf16", "bf16"),
+    (1, 8, 8, 32, True, "f32", "f32"),
+    (1, 1040, 136, 128, False, "f32", "f32"),
+    (5, 520, 72, 32, True, "bf16", "f32"),
+    (19, 904, 200, 64, False, "bf16", "f32"),
+    (150, 512, 136, 128, True, "f32", "f32"),
+]
+
+
+@pytest.mark.parametrize("case", DENSE, ids=lambda c: "-".join(map(str, c)))
+def test_dense(case):
+    T, d_in, d_out, group, zeros, scales, dtype = case
+    dev = device()
+    note(f"w4 dense {case}")
+    packed, s, z = make(1, 1, d_out, d_in, group, zeros, scales)
+    st = pack(packed, s, z, group, scales, dev)
+    x = acts(2, T, d_in, dtype)
+    y = rs.lora_w4_apply(st, torch.from_numpy(x).to(dev).to(DT[dtype]))
+    a = (packed[0], s[0], None if z is None else z[0], group, x)
+    assert_close(y, w4_apply_ref(*a), w4_magnitude_ref(*a), d_in, group, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 9, 40, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_integers_are_exact(T, dtype):
+    """Integer x, scales of powers of two: every sum is exact, so y is the
+    oracle's value rounded once, bit for bit."""
+    dev = device()
+    rng = np.random.default_rng(3)
+    d_in, d_out, group = 648, 328, 32
+    packed, s, z = make(4, 1, d_out, d_in, group, True, "bf16")
+    s = np.exp2(rng.integers(-2, 2, s.shape)).astype(np.float32)
+    x = rng.integers(-4, 5, (T, d_in)).astype(np.float32)
+    y = rs.lora_w4_apply(pack(packed, s, z, group, "bf16", dev), torch.from_numpy(x).to(dev).to(DT[dtype]))
+    want = torch.from_numpy(w4_apply_ref(packed[0], s[0], z[0], group, x)).to(DT[dtype])
+    assert np.array_equal(hbits(y), hbits(want))
+
+
+@pytest.mark.parametrize("T", [1, 20, 260])
+def test_strides_and_neighbours(T):
+    """x and y as column slices of wider buffers, x's other columns NaN; y's
+    other columns and the rows behind the last one keep their values."""
+    dev = device()
+    d_in, d_out, group = 1000, 264, 64
+    packed, s, z = make(5, 1, d_out, d_in, group, False, "bf16")
+    st = pack(packed, s, z, group, "bf16", dev)
+    x = acts(6, T, d_in, "bf16")
+    wide = torch.full((T, d_in + 24), float("nan"), dtype=torch.bfloat16, device=dev)
+    wide[:, 8: 8 + d_in] = torch.from_numpy(x).to(dev)
+    out = torch.full((T + 3, d_out + 32), 7.0, dtype=torch.bfloat16, device=dev)
+    rs.lora_w4_apply(st, wide[:, 8: 8 + d_in], out[:T, 16: 16 + d_out])
+    plain = rs.lora_w4_apply(st, torch.from_numpy(x).to(dev).bfloat16())
+    assert np.array_equal(hbits(out[:T, 16: 16 + d_out].contiguous()), hbits(plain))
+    out[:T, 16: 16 + d_out] = 7.0
+    assert bool((out == 7.0).all())
+
+
+@pytest.mark.parametrize("T", [4, 40, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_bad_row_stays_alone(T, bad):
+    dev = device()
+    d_in, d_out, group = 264, 72, 32
+    packed, s, z = make(7, 1, d_out, d_in, group, True, "bf16")
+    st = pack(packed, s, z, group, "bf16", dev)
+    x = torch.from_numpy(acts(8, T, d_in, "bf16")).to(dev).bfloat16()
+    good = rs.lora_w4_apply(st, x)
+    x[1, 17] = bad
+    y = rs.lora_w4_apply(st, x)
+    keep = [t for t in range(T) if t != 1]
+    assert np.array_equal(hbits(y[keep]), hbits(good[keep]))
+    assert not bool(torch.isfinite(y[1]).any())
+
+
+def test_large_and_small_values():
+    """Rows of very different size in one call: each keeps its own precision."""
+    dev = device()
+    d_in, d_out, group = 520, 136, 64
+    packed, s, z = make(9, 1, d_out, d_in, group, True, "bf16")
+    st = pack(packed, s, z, group, "bf16", dev)
+    for T in (6, 300):
+        x = acts(10, T, d_in, "bf16") * np.exp2(np.linspace(-90, 90, T).round())[:, None].astype(np.float32)
+        x[2] = 0
+        y = rs.lora_w4_apply(st, torch.from_numpy(x).to(dev).bfloat16())
+        a = (packed[0], s[0], z[0], group, x)
+        assert_close(y, w4_apply_ref(*a), w4_magnitude_ref(*a), d_in, group, "bf16")
+
+
+def test_no_rows():
+    dev = device()
+    packed, s, z = make(11, 1, 16, 64, 32, False, "bf16")
+    st = pack(packed, s, z, 32, "bf16", dev)
+    assert rs.lora_w4_apply(st, torch.empty(0, 64, dtype=torch.bfloat16, device=dev)).shape == (0, 16)
+    ids = torch.empty(0, 2, dtype=torch.int32, device=dev)
+    assert rs.lora_w4_apply_experts(st, torch.empty(0, 64, dtype=torch.bfloat16, device=dev), ids).shape == (0, 16)
+
+
+# T, k, E, d_in, d_out, group, zeros, scales, dtype, per choice, combine
+EXPERTS = [
+    (1, 1, 1, 64, 16, 32, False, "bf16", "bf16", False, False),
+    (1, 8, 12, 264, 72, 64, True, "bf16", "bf16", False, False),
+    (1, 8, 12, 264, 72, 64, True, "bf16", "bf16", True, True),
+    (3, 2, 5, 136, 40, 32, True, "f32", "f32", True, True),
+    (7, 3, 4, 520, 104, 128, False, "bf16", "bf16", False, True),
+    (30, 4, 9, 392, 136, 32, True, "bf16", "bf16", True, True),
+    (64, 2, 3, 512, 264, 128, True, "bf16", "bf16", False, False),
+    (50, 3, 200, 136, 40, 64, False, "f32", "bf16", False, True),
+    (300, 4, 6, 264, 200, 64, True, "bf16", "bf16", True, True),
+    (700, 2, 5, 384, 328, 128, False, "bf16", "bf16", False, False),
+    (1500, 3, 17, 136, 72, 32, True, "f32", "bf16", True, False),
+    (120, 4, 8, 264, 72, 64, True, "bf16", "f32", False, True),
+]
+
+
+def experts_case(case, seed, dev, hole=True):
+    T, k, E, d_in, d_out, group, zeros, scales, dtype, per, combine = case
+    rng = np.random.default_rng(seed)
+    packed, s, z = make(seed + 1, E, d_out, d_in, group, zeros, scales)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    if hole and T > 2:
+        ids[1] = -1
+        ids[T - 1, 0], ids[T - 1, k - 1] = E, -5
+        ids[2, :] = ids[2, 0]  # the same expert for every choice
+    w = rng.random((T, k)).astype(np.float32) if combine else None
+    x = acts(seed + 2, T * k if per else T, d_in, dtype)
+    return packed, s, z, x, ids, w
+
+
+@pytest.mark.parametrize("case", EXPERTS, ids=lambda c: "-".join(map(str, c)))
+def test_experts(case):
+    T, k, E, d_in, d_out, group, zeros, scales, dtype, per, combine = case
+    dev = device()
+    note(f"w4 experts {case}")
+    packed, s, z, x, ids, w = experts_case(case, 20, dev)
+    st = pack(packed, s, z, group, scales, dev)
+    xd = torch.from_numpy(x).to(dev).to(DT[dtype])
+    # rows that no choice with an expert reads hold NaN
+    if per:
+        xd[torch.from_numpy(((ids < 0) | (ids >= E)).reshape(-1)).to(dev)] = float("nan")
+    elif T > 2:
+        xd[1] = float("nan")
+    wd = None
+    if combine:
+        wd = torch.from_numpy(w).to(dev)
+        wd[torch.from_numpy((ids < 0) | (ids >= E)).to(dev)] = float("nan")  # whatever its weight
+    y = rs.lora_w4_apply_experts(st, xd, torch.from_numpy(ids).to(dev), wd)
+    ref = experts_ref(packed, s, z, group, x, ids, w)
+    mag = experts_ref(packed, s, z, group, x, ids, w, product=w4_magnitude_ref)
+    assert_close(y, ref, mag, d_in, group, dtype, k=k if combine else 0)
+    if T > 2:
+        empty = y[1:2] if combine else y[k: 2 * k]
+        assert bool((empty == 0).all())
+
+
+def test_one_expert_for_all():
+    """Every row names the same expert (and, once, none at all)."""
+    dev = device()
+    case = (600, 2, 7, 264, 136, 64, True, "bf16", "bf16", False, False)
+    packed, s, z, x, ids, _ = experts_case(case, 30, dev)
+    st, one = pack(packed, s, z, 64, "bf16", dev), pack(packed[3:4], s[3:4], z[3:4], 64, "bf16", dev)
+    xd = torch.from_numpy(x).to(dev).bfloat16()
+    y = rs.lora_w4_apply_experts(st, xd, torch.full((600, 2), 3, dtype=torch.int32, device=dev))
+    want = rs.lora_w4_apply(one, xd.repeat_interleave(2, 0))
+    assert np.array_equal(hbits(y), hbits(want))
+    none = torch.full((600, 2), -1, dtype=torch.int32, device=dev)
+    out = torch.full((1200, 136), 5.0, dtype=torch.bfloat16, device=dev)
+    rs.lora_w4_apply_experts(st, xd, none, None, out)
+    assert bool((out == 0).all())
+    out = torch.full((600, 136), 5.0, dtype=torch.bfloat16, device=dev)
+    rs.lora_w4_apply_experts(st, xd, none, torch.ones(600, 2, device=dev), out)
+    assert bool((out == 0).all())
+
+
+@pytest.mark.parametrize("case", [EXPERTS[2], EXPERTS[5], EXPERTS[8], EXPERTS[9]], ids=lambda c: "-".join(map(str, c)))
+def test_repeated_and_captured(case):
+    """The same call twice is equal bit for bit; so is every replay of a
+    captured one, on new inputs, with eager work on the same store between."""
+    T, k, E, d_in, d_out, group, zeros, scales, dtype, per, combine = case
+    dev = device()
+    packed, s, z, x, ids, w = experts_case(case, 40, dev, hole=False)
+    st = pack(packed, s, z, group, scales, dev)
+    xd = torch.from_numpy(x).to(dev).to(DT[dtype])
+    idd = torch.from_numpy(ids).to(dev)
+    wd = torch.from_numpy(w).to(dev) if combine else None
+    first = rs.lora_w4_apply_experts(st, xd, idd, wd)
+    assert np.array_equal(hbits(first), hbits(rs.lora_w4_apply_experts(st, xd, idd, wd)))
+    out = torch.empty_like(first)
+    nb = rs.lora_w4_workspace_bytes(st, DT[dtype], T, k, combine)
+    ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=dev)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        rs.lora_w4_apply_experts(st, xd, idd, wd, out, ws=ws)
+    for i in range(4):
+        if i:
+            xd.copy_(torch.from_numpy(acts(50 + i, x.shape[0], d_in, dtype)).to(dev))
+            idd.copy_(torch.roll(idd, 1, 0))
+        ws.fill_(255)  # scratch needs no initial value
+        out.fill_(3.0)
+        graph.replay()
+        want = rs.lora_w4_apply_experts(st, xd, idd, wd)
+        torch.cuda.synchronize()
+        assert np.array_equal(hbits(out), hbits(want)), i
+
+
+@pytest.mark.parametrize("T", [1, 24, 400])
+def test_dense_captured_and_on_two_streams(T):
+    dev = device()
+    d_in, d_out, group = 776, 328, 64
+    packed, s, z = make(60, 1, d_out, d_in, group, True, "bf16")
+    st = pack(packed, s, z, group, "bf16", dev)
+    xs = [torch.from_numpy(acts(61 + i, T, d_in, "bf16")).to(dev).bfloat16() for i in range(2)]
+    want = [rs.lora_w4_apply(st, x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for i in range(2):
+        with torch.cuda.stream(streams[i]):
+            got[i] = [rs.lora_w4_apply(st, xs[i]) for _ in range(5)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        for y in got[i]:
+            assert np.array_equal(hbits(y), hbits(want[i]))
+    out = torch.empty_like(want[0])
+    x = xs[0].clone()
+    ws = torch.empty(max(rs.lora_w4_workspace_bytes(st, torch.bfloat16, T), 16), dtype=torch.uint8, device=dev)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rs.lora_w4_apply(st, x, out, ws=ws)
+    for i in (0, 1, 0, 1):
+        x.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(hbits(out), hbits(want[i]))
+
+
+def test_routed_layer():
+    """A layer as it is served: the base projection with the adapters' branch
+    on it, the router, the experts' up product, and their weighted down
+    product, against the oracle fed with the same intermediate values."""
+    from oracle import apply_ref
+    from workloads import make_random_workload
+
+    dev = device()
+    T, d, E, k, inner = 37, 264, 6, 2, 136
+    base = make(70, 1, d, d, 64, False, "bf16")
+    wl = make_random_workload(71, T, 5, d, d, [1, 3, 8, 0, 16], dtype="bf16")
+    st = pack(*base, 64, "bf16", dev)
+    A = [torch.from_numpy(a).to(dev).bfloat16() for a in wl.module.A]
+    B = [torch.from_numpy(b).to(dev).bfloat16() for b in wl.module.B]
+    store = rs.lora_pack_retained(A, B, wl.module.scales)
+    x = torch.from_numpy(wl.x).to(dev).bfloat16()
+    y = rs.lora_w4_apply(st, x)
+    y0 = host(y)
+    rs.lora_apply_batched(store, x, y, ids=torch.from_numpy(wl.ids.astype(np.int32)).to(dev))
+    ref = apply_ref(host(x), wl.ids, wl.module.A, wl.module.B, wl.module.scales, y0=y0)
+    assert np.abs(host(y) - ref).max() <= 2e-2 * np.abs(ref).max()
+
+    gate = torch.from_numpy(acts(72, E, d, "bf16")).to(dev)
+    logits = (y.float() @ gate.t()) / d ** 0.5
+    ids, w = rs.lora_route(logits, k, score="sigmoid", bias=torch.linspace(-0.1, 0.1, E, device=dev))
+    up, down = make(73, E, inner, d, 32, True, "bf16"), make(74, E, d, inner, 32, True, "bf16")
+    u = rs.lora_w4_apply_experts(pack(*up, 32, "bf16", dev), y, ids)
+    idh, wh = ids.cpu().numpy(), w.cpu().numpy()
+    a = (*up, 32, host(y), idh)
+    assert_close(u, experts_ref(*a), experts_ref(*a, product=w4_magnitude_ref), d, 32, "bf16")
+    act = torch.nn.functional.silu(u)
+    out = rs.lora_w4_apply_experts(pack(*down, 32, "bf16", dev), act, ids, w)
+    a = (*down, 32, host(act), idh, wh)
+    assert_close(out, experts_ref(*a), experts_ref(*a, product=w4_magnitude_ref), inner, 32, "bf16", k=k)
+    # experts' ids also group rows for adapters of the experts
+    seg = rs.lora_segment(ids.flatten(), E)
+    assert int(seg.seg_off[E]) == T * k and int(seg.n_invalid[0]) == 0
+
+
+def test_refused_on_the_gpu():
+    dev = device()
+    packed, s, z = make(80, 2, 16, 64, 32, False, "bf16")
+    st = pack(packed, s, z, 32, "bf16", dev)
+    x = torch.zeros(4, 64, dtype=torch.bfloat16, device=dev)
+    with pytest.raises(rs.LoraError):
+        rs.lora_w4_apply(st, x)  # two matrices
+    ids = torch.zeros(4, 2, dtype=torch.int32, device=dev)
+    with pytest.raises(ValueError, match="GPU|cpu"):
+        rs.lora_w4_apply_experts(st, x.cpu(), ids)
+    with pytest.raises(ValueError, match="ids"):
+        rs.lora_w4_apply_experts(st, x, ids.long())
+    with pytest.raises(ValueError, match="x must"):
+        rs.lora_w4_apply_experts(st, x[:3], ids)
+    with pytest.raises(ValueError, match="weights"):
+        rs.lora_w4_apply_experts(st, x, ids, torch.ones(4, 2, dtype=torch.bfloat16, device=dev))
+    with pytest.raises(ValueError, match="y must"):
+        rs.lora_w4_apply_experts(st, x, ids, None, torch.zeros(4, 16, dtype=torch.bfloat16, device=dev))
+    with pytest.raises(rs.LoraError):
+        rs.lora_w4_apply_experts(st, torch.zeros(4, 68, dtype=torch.bfloat16, device=dev)[:, 2:66], ids)
