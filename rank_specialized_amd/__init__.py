@@ -635,6 +635,24 @@ class W4Store:
         return W4Store(c, codes, params)
 
 
+class _Device:
+    """Makes `index` the current device for a call, where it is not already."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
 def _on(device: torch.device, **tensors) -> None:
     """Every tensor given is on `device`, a GPU."""
     if device.type != "cuda":
@@ -695,7 +713,7 @@ def lora_w4_pack(q: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Te
     codes = torch.empty(cb, dtype=torch.uint8, device=q.device)
     params = torch.empty(pb, dtype=torch.uint8, device=q.device)
     c = L.lora_w4_store()
-    with torch.cuda.device(q.device):
+    with _Device(q.device.index):
         L.check("lora_w4_pack", L.lib().lora_w4_pack(C.byref(c), n, d_in, d_out, group, _p(q), _p(scales), sd,
                                                      _p(zeros), codes.data_ptr(), params.data_ptr(), _stream(q)))
     return W4Store(c, codes, params)
@@ -732,7 +750,7 @@ def lora_w4_apply(store: W4Store, x: torch.Tensor, y: Optional[torch.Tensor] = N
     y = _w4_out(y, T, store, x)
     _on(store.codes.device, x=x, y=y, ws=ws)
     ws = _w4_ws(store, x, T, 0, False, ws)
-    with torch.cuda.device(x.device):
+    with _Device(x.device.index):
         L.check("lora_w4_apply", L.lib().lora_w4_apply(
             store.ref(), dt, _p(x), ldx, _p(y), _ld(y, "y"), T, _p(ws), ws.numel() if ws is not None else 0, _stream(x)))
     return y
@@ -759,7 +777,7 @@ def lora_w4_apply_experts(store: W4Store, x: torch.Tensor, ids: torch.Tensor, we
     y = _w4_out(y, T if weights is not None else T * k, store, x)
     _on(store.codes.device, x=x, ids=ids, weights=weights, y=y, ws=ws)
     ws = _w4_ws(store, x, T, k, weights is not None, ws)
-    with torch.cuda.device(x.device):
+    with _Device(x.device.index):
         L.check("lora_w4_apply_experts", L.lib().lora_w4_apply_experts(
             store.ref(), dt, _p(x), ldx, int(x.shape[0] != T), _p(y), _ld(y, "y"), T, k, _p(ids), _p(weights),
             _p(ws), ws.numel() if ws is not None else 0, _stream(x)))
@@ -794,7 +812,7 @@ def lora_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Op
     if weights.shape != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
         raise ValueError("weights must be a contiguous float32 [T, k]")
     _on(logits.device, bias=bias, ids=ids, weights=weights)
-    with torch.cuda.device(logits.device):
+    with _Device(logits.device.index):
         L.check("lora_route", L.lib().lora_route(
             _p(logits), ldl, dt, T, E, k, _SCORES[score], _p(bias), int(groups), int(top_groups), int(renormalize),
             float(scale), _p(ids), _p(weights), _stream(logits)))

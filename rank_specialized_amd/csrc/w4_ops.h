@@ -8,21 +8,41 @@ namespace lora {
 // Four operand dwords (two numbers each) of a lane's eight codes: each half
 // of `magic` is 16.0 in bf16 (0x4180) or 128.0 in f16 (0x5800), whose last
 // bits the code takes: 16 + q, 128 + q, exact.  `mask` and `magic` come from
-// w4_constant, so that each step is one v_and_or_b32.
+// w4_scalar and w4_vector, so that each step is one v_and_or_b32.
 __device__ __forceinline__ uint4 w4_expand(uint32_t w, uint32_t mask, uint32_t magic) {
   return make_uint4((w & mask) | magic, ((w >> 4) & mask) | magic, ((w >> 8) & mask) | magic,
                     (__builtin_amdgcn_alignbit(w, w, 12) & mask) | magic);
 }
-// A constant the compiler takes for a value: two literals would not fit one
-// v_and_or_b32, and it would use two instructions.  (The and-or itself stays
-// out of inline assembly: a matrix instruction must not read a register
-// within two wait states of its write, and the compiler cannot see one there.)
-__device__ __forceinline__ uint32_t w4_constant(uint32_t v) {
+// Constants the compiler takes for values, one in a scalar and one in a vector
+// register: v_and_or_b32 takes no literals and one scalar operand, and would
+// be two instructions otherwise.  (The and-or itself stays out of inline
+// assembly: a matrix instruction must not read a register within two wait
+// states of its write, and the compiler cannot see one there.)
+__device__ __forceinline__ uint32_t w4_scalar(uint32_t v) {
   uint32_t r;
   asm("s_mov_b32 %0, %1" : "=s"(r) : "i"(v));
   return r;
 }
+__device__ __forceinline__ uint32_t w4_vector(uint32_t v) {
+  uint32_t r;
+  asm("v_mov_b32 %0, %1" : "=v"(r) : "s"(w4_scalar(v)));
+  return r;
+}
 constexpr uint32_t kCodeMask = 0x00780078u;
+// q - z itself, exact in bf16 (at most five bits): the eight numbers widened,
+// 16 + z taken off, the halves put together again (27 instructions for eight
+// codes against 7).
+__device__ __forceinline__ uint4 w4_expand_exact(uint32_t w, uint32_t mask, uint32_t magic, float zero16) {
+  const uint4 v = w4_expand(w, mask, magic);
+  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+  uint32_t out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = bf16_lo(in[i]) - zero16, hi = bf16_hi(in[i]) - zero16;
+    out[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
 constexpr uint32_t kMagicBf16 = 0x41804180u;
 constexpr uint32_t kMagicF16 = 0x58005800u;
 
@@ -98,5 +118,70 @@ struct XFrag<F32> {
     for (int q = 0; q < 3; ++q) o[q] = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
   }
 };
+
+// What the row kernels are called with.
+struct W4RowsArgs {
+  const char* codes;
+  const char* params;
+  int64_t code_stride, param_stride;  // bytes per matrix
+  int n, k_tiles, row_tiles, d_in, d_out;
+  const char* x;
+  int64_t ldx_bytes;
+  int x_div;
+  char* y;  // rows of the output type, or of float32 (f32_out)
+  int64_t ldy_bytes;
+  int R, k;
+  const int32_t* ids;    // nullptr: matrix 0
+  const float* weights;  // a token's rows summed by one workgroup
+  int by_row;            // routed: blockIdx.y is a row (the first row of its matrix works), else a matrix
+  int f32_out;
+  int row_cap;           // rows that the kernel holds in LDS at a time
+};
+
+constexpr int kListMax = 4096;  // rows of a routed call that are listed at a time
+
+template <typename E>
+__device__ __forceinline__ void w4_store(char* row, int o, float v, int f32_out) {
+  if (E::kBytes == 4 || f32_out) reinterpret_cast<float*>(row)[o] = v;
+  else reinterpret_cast<uint16_t*>(row)[o] = (uint16_t)f32_to_bf16(v);
+}
+
+// The rows of [win, win + kListMax) whose id is e (or, `none`, outside
+// [0, n)), ascending, into `list`; returns their number.  Per chunk of 64 W
+// rows, each wave counts its 64 by ballot and the waves' counts are added up
+// in order.
+template <int W>
+__device__ __forceinline__ int w4_rows_of(const W4RowsArgs& p, int e, bool none, int win, uint16_t* list, int* s_cnt) {
+  const int tid = (int)threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int end = min(p.R, win + kListMax);
+  int cnt = 0;
+  for (int r0 = win; r0 < end; r0 += 64 * W) {
+    const int r = r0 + tid;
+    const int id = r < end ? p.ids[r] : 0;
+    const bool hit = r < end && (none ? (unsigned)id >= (unsigned)p.n : id == e);
+    const uint64_t mask = __ballot(hit);
+    if (lane == 0) s_cnt[w] = __popcll(mask);
+    __syncthreads();
+    int before = cnt, total = cnt;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      before += i < w ? s_cnt[i] : 0;
+      total += s_cnt[i];
+    }
+    if (hit) list[before + __popcll(mask & lanemask_lt())] = (uint16_t)(r - win);
+    cnt = total;
+    __syncthreads();
+  }
+  return cnt;
+}
+
+// Empty sums: outputs [o0, o0 + width) of `cnt` listed rows.
+template <typename E>
+__device__ __forceinline__ void w4_zero_rows(const W4RowsArgs& p, int win, const uint16_t* list, int cnt, int o0, int width) {
+  for (int i = (int)threadIdx.x; i < cnt * width; i += (int)blockDim.x) {
+    const int o = o0 + i % width;
+    if (o < p.d_out) w4_store<E>(p.y + (int64_t)(win + list[i / width]) * p.ldy_bytes, o, 0.f, p.f32_out);
+  }
+}
 
 }  // namespace lora

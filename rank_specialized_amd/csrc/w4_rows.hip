@@ -21,7 +21,9 @@
 // layout, and its multiple is the accumulator that the group's products
 // start from.  All products are exact in float32 and only the sums round;
 // 16 is the smallest base that bf16 can hold with a step of one code, which
-// keeps the cancelled part small (about three times the result).
+// keeps the cancelled part small (about three times the result).  Float32
+// rows, which take three products per step anyway, are multiplied with q - z
+// itself: more work per code, no cancellation.
 #include "host_util.h"
 #include "w4_kernels.h"
 #include "w4_ops.h"
@@ -29,51 +31,29 @@
 namespace lora {
 namespace {
 
-constexpr int kListMax = 4096;  // rows of a routed call that this kernel takes
-
-struct W4RowsArgs {
-  const char* codes;
-  const char* params;
-  int64_t code_stride, param_stride;  // bytes per matrix
-  int n, k_tiles, row_tiles, d_in, d_out;
-  const char* x;
-  int64_t ldx_bytes;
-  int x_div;
-  char* y;            // rows of the output type, or of float32 (f32_out)
-  int64_t ldy_bytes;
-  int R, k;
-  const int32_t* ids;     // nullptr: matrix 0
-  const float* weights;   // COMBINE only
-  int by_row;             // routed: blockIdx.y is a row (the first row of its matrix works), else a matrix
-  int f32_out;
-};
-
-template <typename E, int KIND, int SUB, int RT, int NT, bool COMBINE>
+template <typename E, int KIND, int SUB, int RT, int NT>
 struct Slot {
   uint4 code[RT];
   W4Params<KIND, SUB> par[RT];
   XFrag<E> x[NT][4];
 };
 
-template <typename E>
-__device__ __forceinline__ void store_out(char* row, int o, float v) {
-  if constexpr (E::kBytes == 2) reinterpret_cast<uint16_t*>(row)[o] = (uint16_t)f32_to_bf16(v);
-  else reinterpret_cast<float*>(row)[o] = v;
-}
-
-template <typename E, int KIND, int SUB, int RT, int NT, int U, int W, bool COMBINE>
-__global__ __launch_bounds__(64 * W) void w4_rows_kernel(const W4RowsArgs p) {
+template <typename E, int KIND, int SUB, int RT, int NT, int U, int W>
+__global__ __launch_bounds__(64 * W) __attribute__((amdgpu_waves_per_eu(2)))
+void w4_rows_kernel(const W4RowsArgs p) {
   constexpr int kTok = 16 * NT;
   constexpr int kStepsPerSub = 4 / SUB;
+  constexpr bool kExact = XFrag<E>::kParts > 1;
   constexpr int kPad = 17;  // LDS row stride of a 16 x 16 block
   __shared__ float red[W][RT][NT][16 * kPad];
-  __shared__ uint16_t list[COMBINE ? 1 : kListMax];
+  __shared__ uint16_t list[kListMax];
   __shared__ int s_cnt[W + 1];
-  const int tid = (int)threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: addresses of codes stay scalar
   const int col = lane & 15, h = lane >> 4;
   const int rt0 = (int)blockIdx.x * RT;
 
-  const bool listed = !COMBINE && p.ids != nullptr;
+  const bool listed = p.ids != nullptr;
   const int self = listed && p.by_row ? (int)blockIdx.y : -1;
   int e = 0;
   bool none = false;
@@ -81,59 +61,29 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(const W4RowsArgs p) {
     e = p.by_row ? p.ids[self] : (int)blockIdx.y;
     none = (unsigned)e >= (unsigned)p.n;  // rows without a matrix (by matrix: one workgroup row for them)
   }
-  const int tiles = (COMBINE ? p.k : 1) * p.k_tiles;
-  const int last_chunk = p.d_in - 8;
+  const int tiles = p.k_tiles;
+  const int last_chunk = p.d_in - 8, k_full = p.d_in / kW4K;
+  const uint32_t lane16 = 16 * lane, lane_par = col * W4Params<KIND, SUB>::kBytes;
   const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-  const uint32_t mask = w4_constant(kCodeMask), magic = w4_constant(kMagicBf16);
+  const uint32_t mask = w4_scalar(kCodeMask), magic = w4_vector(kMagicBf16);
   int rt_of[RT];
 #pragma unroll
   for (int a = 0; a < RT; ++a) rt_of[a] = min(rt0 + a, p.row_tiles - 1);
 
-  // ---- the rows: one token's k rows, each with its own matrix (COMBINE);
-  // a run of rows (one matrix); or the rows whose id is e, found in windows
-  // of kListMax rows.
+  // ---- the rows: a run of rows (one matrix), or the rows whose id is e,
+  // found in windows of kListMax rows.
   for (int win = 0; win < (listed ? p.R : 1); win += kListMax) {
   int base = 0, m_all = 0;
-  if constexpr (COMBINE) {
-    base = (int)blockIdx.y * p.k;
-    m_all = 1;
-  } else if (!listed) {
+  if (!listed) {
     base = (int)blockIdx.y * kTok;
     m_all = min(kTok, p.R - base);
   } else {
-    // Ascending: per chunk of 64 W rows, each wave counts its 64 by ballot
-    // and the waves' counts are added up in order.
-    const int end = min(p.R, win + kListMax);
-    int cnt = 0;
-    for (int r0 = win; r0 < end; r0 += 64 * W) {
-      const int r = r0 + tid;
-      const int id = r < end ? p.ids[r] : 0;
-      const bool hit = r < end && (none ? (unsigned)id >= (unsigned)p.n : id == e);
-      const uint64_t mask = __ballot(hit);
-      if (lane == 0) s_cnt[w] = __popcll(mask);
-      __syncthreads();
-      int before = cnt, total = cnt;
-#pragma unroll
-      for (int i = 0; i < W; ++i) {
-        before += i < w ? s_cnt[i] : 0;
-        total += s_cnt[i];
-      }
-      if (hit) list[before + __popcll(mask & lanemask_lt())] = (uint16_t)(r - win);
-      cnt = total;
-      __syncthreads();
-    }
+    int cnt = w4_rows_of<W>(p, e, none, win, list, s_cnt);
     // By row (one window): an earlier row's workgroup has this matrix.
     if (p.by_row && (int)list[0] != self) return;
     base = win;
-    if (none) {  // empty sums
-      for (int i = tid; i < cnt * 16 * RT; i += 64 * W) {
-        const int o = 16 * rt0 + i % (16 * RT);
-        if (o < p.d_out) {
-          char* row = p.y + (int64_t)(win + list[i / (16 * RT)]) * p.ldy_bytes;
-          if (p.f32_out) reinterpret_cast<float*>(row)[o] = 0.f;
-          else store_out<E>(row, o, 0.f);
-        }
-      }
+    if (none) {
+      w4_zero_rows<E>(p, win, list, cnt, 16 * rt0, 16 * RT);
       cnt = 0;
     }
     m_all = cnt;
@@ -147,7 +97,7 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(const W4RowsArgs p) {
     for (int t = 0; t < NT; ++t) {
       const int i = m0 + min(16 * t + col, m - 1);
       const int r = base + (listed ? (int)list[i] : i);
-      xrow[t] = p.x + (int64_t)(r / p.x_div) * p.ldx_bytes;
+      xrow[t] = p.x + (int64_t)(r / p.x_div) * p.ldx_bytes + 8 * h * E::kBytes;
     }
     f32x4_t acc[RT][NT];
 #pragma unroll
@@ -155,50 +105,32 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(const W4RowsArgs p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t) acc[a][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    Slot<E, KIND, SUB, RT, NT, COMBINE> slot[U];
-    // Tile i of the wave's turn: COMBINE runs through the k matrices of the
-    // token one after the other (a row without a matrix: weight 0, matrix 0).
-    auto locate = [&](int i, int& kt, int64_t& mat, float& wt, const char*& xr) {
-      if constexpr (COMBINE) {
-        const int j = i / p.k_tiles;
-        kt = i - j * p.k_tiles;
-        const int r = base + j;
-        const int id = p.ids[r];
-        const bool ok = (unsigned)id < (unsigned)p.n;
-        mat = ok ? id : 0;
-        wt = ok ? p.weights[r] : 0.f;
-        xr = p.x + (int64_t)(r / p.x_div) * p.ldx_bytes;
-      } else {
-        kt = i;
-        mat = e;
-        wt = 1.f;
-        xr = nullptr;
-      }
-    };
-    float slot_w[U];
-    bool slot_ok[U];
-    auto fetch = [&](int u, int i) {
-      int kt;
-      int64_t mat;
-      const char* xr;
-      locate(i, kt, mat, slot_w[u], xr);
-      slot_ok[u] = !COMBINE || (unsigned)p.ids[base + i / p.k_tiles] < (unsigned)p.n;
-      const char* cb = p.codes + mat * p.code_stride + (int64_t)kt * kW4TileBytes + 16 * lane;
-      const char* pb = p.params + mat * p.param_stride +
-                       ((int64_t)kt * kW4Rows + col) * W4Params<KIND, SUB>::kBytes;
+    Slot<E, KIND, SUB, RT, NT> slot[U];
+    const char* cb = p.codes + e * p.code_stride;
+    const char* pb = p.params + e * p.param_stride;
+    auto fetch = [&](int u, int kt) {
 #pragma unroll
       for (int a = 0; a < RT; ++a) {
-        const int64_t at = (int64_t)rt_of[a] * p.k_tiles;
-        slot[u].code[a] = ld16_stream(cb + at * kW4TileBytes);
-        slot[u].par[a].load(pb + at * kW4Rows * W4Params<KIND, SUB>::kBytes);
+        const int64_t at = (int64_t)rt_of[a] * p.k_tiles + kt;
+        slot[u].code[a] = ld16_stream(cb + at * kW4TileBytes + lane16);
+        slot[u].par[a].load(pb + at * kW4Rows * W4Params<KIND, SUB>::kBytes + lane_par);
       }
+      if (kt < k_full) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
+          const char* xk = xrow[t] + (int64_t)kt * (kW4K * E::kBytes);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = min(kW4K * kt + 32 * j + 8 * h, last_chunk);
-          slot[u].x[t][j].load((COMBINE ? xr : xrow[t]) + (int64_t)k * E::kBytes);
+          for (int j = 0; j < 4; ++j) slot[u].x[t][j].load(xk + 32 * j * E::kBytes);
         }
+      } else {  // the tile that d_in ends in: chunks past the end meet codes equal to their zero point
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = min(kW4K * kt + 32 * j + 8 * h, last_chunk) - 8 * h;
+            slot[u].x[t][j].load(xrow[t] + (int64_t)k * E::kBytes);
+          }
+      }
     };
     auto compute = [&](int u) {
 #pragma unroll
@@ -211,8 +143,7 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(const W4RowsArgs p) {
 #pragma unroll
           for (int j = 0; j < kStepsPerSub; ++j) {
             slot[u].x[t][s * kStepsPerSub + j].parts(xp[t][j]);
-#pragma unroll
-            for (int q = 0; q < XFrag<E>::kParts; ++q) xs[t] = mfma_bf16_16x16x32(xp[t][j][q], ones, xs[t]);
+            if constexpr (!kExact) xs[t] = mfma_bf16_16x16x32(xp[t][j][0], ones, xs[t]);
           }
         }
 #pragma unroll
@@ -220,14 +151,16 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(const W4RowsArgs p) {
           const uint32_t cw[4] = {slot[u].code[a].x, slot[u].code[a].y, slot[u].code[a].z, slot[u].code[a].w};
           uint4 b[kStepsPerSub];
 #pragma unroll
-          for (int j = 0; j < kStepsPerSub; ++j) b[j] = w4_expand(cw[s * kStepsPerSub + j], mask, magic);
-          const float sc = COMBINE ? slot[u].par[a].scale(s) * slot_w[u] : slot[u].par[a].scale(s);
+          for (int j = 0; j < kStepsPerSub; ++j)
+            b[j] = kExact ? w4_expand_exact(cw[s * kStepsPerSub + j], mask, magic, slot[u].par[a].zero16(s))
+                          : w4_expand(cw[s * kStepsPerSub + j], mask, magic);
+          const float sc = slot[u].par[a].scale(s);
           const float zz = -slot[u].par[a].zero16(s);
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
             f32x4_t c;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) c[v] = zz * xs[t][v];
+            for (int v = 0; v < 4; ++v) c[v] = kExact ? 0.f : zz * xs[t][v];
 #pragma unroll
             for (int j = 0; j < kStepsPerSub; ++j)
 #pragma unroll
@@ -245,7 +178,7 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(const W4RowsArgs p) {
     for (int i0 = w; i0 < tiles; i0 += U * W) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (i0 + u * W < tiles && slot_ok[u]) compute(u);
+        if (i0 + u * W < tiles) compute(u);
         if (i0 + U * W < tiles) fetch(u, min(i0 + (u + U) * W, tiles - 1));
       }
     }
@@ -265,10 +198,9 @@ __global__ __launch_bounds__(64 * W) void w4_rows_kernel(const W4RowsArgs p) {
       float v = 0.f;
 #pragma unroll
       for (int ww = 0; ww < W; ++ww) v += red[ww][a][row >> 4][(row & 15) * kPad + o16];
-      const int r = COMBINE ? (int)blockIdx.y : base + (listed ? (int)list[m0 + row] : row);
+      const int r = base + (listed ? (int)list[m0 + row] : row);
       char* yrow = p.y + (int64_t)r * p.ldy_bytes;
-      if (p.f32_out) reinterpret_cast<float*>(yrow)[o] = v;
-      else store_out<E>(yrow, o, v);
+      w4_store<E>(yrow, o, v, p.f32_out);
     }
     __syncthreads();  // the sums (and, in a further window, the list) are written again
   }
@@ -300,33 +232,32 @@ __global__ __launch_bounds__(256) void w4_combine_kernel(const float* __restrict
     *reinterpret_cast<f32x4_t*>(dst) = s;
 }
 
-template <typename E, int KIND, int SUB, int RT, int NT, int U, int W, bool COMBINE>
+template <typename E, int KIND, int SUB, int RT, int NT, int U, int W>
 hipError_t launch_one(const W4RowsArgs& a, unsigned gy, hipStream_t stream) {
   const dim3 grid((unsigned)((a.row_tiles + RT - 1) / RT), gy);
-  hipLaunchKernelGGL((w4_rows_kernel<E, KIND, SUB, RT, NT, U, W, COMBINE>), grid, dim3(64 * W), 0, stream, a);
+  hipLaunchKernelGGL((w4_rows_kernel<E, KIND, SUB, RT, NT, U, W>), grid, dim3(64 * W), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename E, int KIND, int SUB>
-hipError_t launch_rows(const W4RowsArgs& a, int rows_per, unsigned gy, bool combine, hipStream_t stream) {
+hipError_t launch_rows(const W4RowsArgs& a, int rows_per, unsigned gy, hipStream_t stream) {
   constexpr int kU = E::kBytes == 2 ? 4 : 2;
-  if (combine) return launch_one<E, KIND, SUB, 1, 1, kU, 8, true>(a, gy, stream);
-  if (rows_per <= 16) return launch_one<E, KIND, SUB, 1, 1, kU, 8, false>(a, gy, stream);
-  return launch_one<E, KIND, SUB, 2, 2, 1, 4, false>(a, gy, stream);
+  if (rows_per <= 16) return launch_one<E, KIND, SUB, 1, 1, kU, 8>(a, gy, stream);
+  return launch_one<E, KIND, SUB, 2, 2, 1, 4>(a, gy, stream);
 }
 
 template <typename E>
-hipError_t launch_kind(const W4RowsArgs& a, int kind, int sub, int rows_per, unsigned gy, bool combine, hipStream_t st) {
+hipError_t launch_kind(const W4RowsArgs& a, int kind, int sub, int rows_per, unsigned gy, hipStream_t st) {
   switch (kind * 8 + sub) {
-    case kW4Bf16 * 8 + 1: return launch_rows<E, kW4Bf16, 1>(a, rows_per, gy, combine, st);
-    case kW4Bf16 * 8 + 2: return launch_rows<E, kW4Bf16, 2>(a, rows_per, gy, combine, st);
-    case kW4Bf16 * 8 + 4: return launch_rows<E, kW4Bf16, 4>(a, rows_per, gy, combine, st);
-    case kW4Bf16Zero * 8 + 1: return launch_rows<E, kW4Bf16Zero, 1>(a, rows_per, gy, combine, st);
-    case kW4Bf16Zero * 8 + 2: return launch_rows<E, kW4Bf16Zero, 2>(a, rows_per, gy, combine, st);
-    case kW4Bf16Zero * 8 + 4: return launch_rows<E, kW4Bf16Zero, 4>(a, rows_per, gy, combine, st);
-    case kW4F32 * 8 + 1: return launch_rows<E, kW4F32, 1>(a, rows_per, gy, combine, st);
-    case kW4F32 * 8 + 2: return launch_rows<E, kW4F32, 2>(a, rows_per, gy, combine, st);
-    default: return launch_rows<E, kW4F32, 4>(a, rows_per, gy, combine, st);
+    case kW4Bf16 * 8 + 1: return launch_rows<E, kW4Bf16, 1>(a, rows_per, gy, st);
+    case kW4Bf16 * 8 + 2: return launch_rows<E, kW4Bf16, 2>(a, rows_per, gy, st);
+    case kW4Bf16 * 8 + 4: return launch_rows<E, kW4Bf16, 4>(a, rows_per, gy, st);
+    case kW4Bf16Zero * 8 + 1: return launch_rows<E, kW4Bf16Zero, 1>(a, rows_per, gy, st);
+    case kW4Bf16Zero * 8 + 2: return launch_rows<E, kW4Bf16Zero, 2>(a, rows_per, gy, st);
+    case kW4Bf16Zero * 8 + 4: return launch_rows<E, kW4Bf16Zero, 4>(a, rows_per, gy, st);
+    case kW4F32 * 8 + 1: return launch_rows<E, kW4F32, 1>(a, rows_per, gy, st);
+    case kW4F32 * 8 + 2: return launch_rows<E, kW4F32, 2>(a, rows_per, gy, st);
+    default: return launch_rows<E, kW4F32, 4>(a, rows_per, gy, st);
   }
 }
 
@@ -354,12 +285,16 @@ hipError_t launch_w4_rows(const W4Call& c, hipStream_t stream) {
   a.R = c.R;
   a.k = c.k;
   a.ids = c.ids;
-  a.weights = c.weights;
   int rows_per = c.R;
   unsigned gy;
   const bool combine = c.plan.sum_in_kernel;
+  a.weights = combine ? c.weights : nullptr;
+  const int cap = w4_few_rows(c.dtype, s.d_in);
+  a.row_cap = cap < 16 ? cap : 16;
   if (combine) {
     gy = (unsigned)(c.R / c.k);
+    a.row_cap = c.x_div == 1 ? c.k : 1;
+    return launch_w4_few(a, c.dtype, kind, sub, gy, stream);
   } else if (c.ids != nullptr) {
     if (c.weights != nullptr) {
       a.y = c.ws + c.plan.part;
@@ -372,8 +307,13 @@ hipError_t launch_w4_rows(const W4Call& c, hipStream_t stream) {
   } else {
     gy = (unsigned)((c.R + (c.R <= 16 ? 15 : 31)) / (c.R <= 16 ? 16 : 32));
   }
-  return c.dtype == LORA_DTYPE_BF16 ? launch_kind<BF16>(a, kind, sub, rows_per, gy, combine, stream)
-                                    : launch_kind<F32>(a, kind, sub, rows_per, gy, combine, stream);
+  if (rows_per <= 16 && a.row_cap >= (rows_per < 16 ? rows_per : 16)) {
+    const int want = rows_per + 3 < c.R ? rows_per + 3 : c.R;
+    a.row_cap = a.row_cap < want ? a.row_cap : want;
+    return launch_w4_few(a, c.dtype, kind, sub, c.ids ? gy : (unsigned)((c.R + a.row_cap - 1) / a.row_cap), stream);
+  }
+  return c.dtype == LORA_DTYPE_BF16 ? launch_kind<BF16>(a, kind, sub, rows_per, gy, stream)
+                                    : launch_kind<F32>(a, kind, sub, rows_per, gy, stream);
 }
 
 hipError_t launch_w4_combine(const W4Call& c, const float* part, hipStream_t stream) {
@@ -390,7 +330,7 @@ hipError_t launch_w4_combine(const W4Call& c, const float* part, hipStream_t str
 }
 
 hipError_t launch_w4(const W4Call& c, hipStream_t stream) {
-  hipError_t e = launch_w4_rows(c, stream);
+  hipError_t e = c.plan.bm > 0 ? launch_w4_gemm(c, stream) : launch_w4_rows(c, stream);
   if (e == hipSuccess && c.weights != nullptr && !c.plan.sum_in_kernel)
     e = launch_w4_combine(c, reinterpret_cast<const float*>(c.ws + c.plan.part), stream);
   return e;
