@@ -35,14 +35,14 @@ def w4_apply_ref(packed, scales, zeros, group: int, x) -> np.ndarray:
 
 
 def w4_magnitude_ref(packed, scales, zeros, group: int, x) -> np.ndarray:
-    """sum_k |s| (16 + q + 16 + z) |x|: what the products and their correction
+    """sum_k |s| (32 + q + 32 + z) |x|: what the products and their correction
     add up to in absolute value, the measure of a float32 sum's error."""
     q = unpack_ref(packed)
     m = np.empty(q.shape, np.float64)
     for g in range(scales.shape[-1]):
         at = slice(g * group, min(q.shape[-1], (g + 1) * group))
         z = 8 if zeros is None else zeros[..., g: g + 1].astype(np.int64)
-        m[..., at] = (32 + q[..., at] + z) * np.abs(scales[..., g: g + 1].astype(np.float64))
+        m[..., at] = (64 + q[..., at] + z) * np.abs(scales[..., g: g + 1].astype(np.float64))
     return np.abs(np.asarray(x, np.float64)) @ m.T
 
 

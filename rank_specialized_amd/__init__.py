@@ -608,24 +608,17 @@ class W4Store:
     codes: torch.Tensor
     params: torch.Tensor
 
-    @property
-    def n(self) -> int:
-        return self.c.n
-
-    @property
-    def d_in(self) -> int:
-        return self.c.d_in
-
-    @property
-    def d_out(self) -> int:
-        return self.c.d_out
-
-    @property
-    def group(self) -> int:
-        return self.c.group
+    def __post_init__(self):
+        # Plain attributes: a decode step's call is short enough for the
+        # struct's accessors to show.
+        c = self.c
+        self.n, self.d_in, self.d_out, self.group = c.n, c.d_in, c.d_out, c.group
+        self.device_index = self.codes.get_device()
+        self._ref = C.byref(c)
+        self._ws_bytes = {}
 
     def ref(self):
-        return C.byref(self.c)
+        return self._ref
 
     def clone(self) -> "W4Store":
         """An independent copy in fresh device memory (same layout)."""
@@ -635,44 +628,51 @@ class W4Store:
         return W4Store(c, codes, params)
 
 
-class _Device:
-    """Makes `index` the current device for a call, where it is not already."""
-
-    __slots__ = ("index", "before")
-
-    def __init__(self, index: int):
-        self.index = index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+# The handle of a device's current stream, without a Stream object around it
+# where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(device: torch.device, **tensors) -> None:
-    """Every tensor given is on `device`, a GPU."""
-    if device.type != "cuda":
+def _call(name: str, index: int, *args) -> None:
+    """The library's `name` on the current stream of device `index`, which is
+    made the current device for the call."""
+    fn = getattr(L.lib(), name)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        L.check(name, status)
+
+
+def _same_device(index: int, **tensors) -> None:
+    """Every tensor given is on GPU `index`."""
+    if index < 0:
         raise ValueError("tensors must be on a GPU")
     for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
 def _ld(t: torch.Tensor, name: str) -> int:
-    """Row stride of a 2-D tensor; of at most one row, its length (its stride is then any number)."""
-    if t.dim() != 2 or t.shape[0] > 1 or (t.shape[0] == 1 and t.shape[1] > 1 and t.stride(1) != 1):
-        return _rows(t, name)
-    return t.shape[1]
+    """Row stride of a 2-D tensor with unit column stride; of at most one row,
+    its length (its stride is then any number)."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if rows > 0 and cols > 1 and step != 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    return ld if rows > 1 else cols
 
 
 def _dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _DTYPES:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{name} must be bfloat16 or float32")
-    return _DTYPES[t.dtype]
+    return dt
 
 
 def lora_w4_bytes(n: int, d_in: int, d_out: int, group: int, scale_dtype: torch.dtype, has_zeros: bool):
@@ -706,16 +706,16 @@ def lora_w4_pack(q: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Te
     if zeros is not None and (zeros.shape != shape or zeros.dtype != torch.uint8):
         raise ValueError(f"zeros must be uint8 {shape}")
     sd = _dtype(scales, "scales")
-    _on(q.device, scales=scales, zeros=zeros)
+    index = q.get_device()
+    _same_device(index, scales=scales, zeros=zeros)
     q, scales = q.contiguous(), scales.contiguous()
     zeros = zeros.contiguous() if zeros is not None else None
     cb, pb = lora_w4_bytes(n, d_in, d_out, group, scales.dtype, zeros is not None)
     codes = torch.empty(cb, dtype=torch.uint8, device=q.device)
     params = torch.empty(pb, dtype=torch.uint8, device=q.device)
     c = L.lora_w4_store()
-    with _Device(q.device.index):
-        L.check("lora_w4_pack", L.lib().lora_w4_pack(C.byref(c), n, d_in, d_out, group, _p(q), _p(scales), sd,
-                                                     _p(zeros), codes.data_ptr(), params.data_ptr(), _stream(q)))
+    _call("lora_w4_pack", index, C.byref(c), n, d_in, d_out, group, _p(q), _p(scales), sd, _p(zeros),
+          codes.data_ptr(), params.data_ptr())
     return W4Store(c, codes, params)
 
 
@@ -724,36 +724,45 @@ def lora_w4_workspace_bytes(store: W4Store, dtype: torch.dtype, T: int, k: int =
     return int(L.lib().lora_w4_workspace_bytes(store.ref(), _DTYPES[dtype], int(T), int(k), int(weighted)))
 
 
-def _w4_out(y, rows: int, store: W4Store, x: torch.Tensor) -> torch.Tensor:
+def _w4_run(name: str, store: W4Store, x: torch.Tensor, rows: int, y, T: int, k: int, ids, weights, ws, middle):
+    """The part the two products share: y and the workspace, the checks, the call."""
+    dt, ldx, index = _dtype(x, "x"), _ld(x, "x"), store.device_index
+    if x.shape[1] != store.d_in:
+        raise ValueError("x must have d_in columns")
+    if x.get_device() != index:
+        _same_device(index, x=x)
     if y is None:
-        return torch.empty(rows, store.d_out, dtype=x.dtype, device=x.device)
-    if y.shape != (rows, store.d_out) or y.dtype != x.dtype:
-        raise ValueError(f"y must be [{rows}, {store.d_out}] of x's dtype")
-    return y
-
-
-def _w4_ws(store: W4Store, x: torch.Tensor, T: int, k: int, weighted: bool, ws):
+        ldy = store.d_out
+        y = torch.empty(rows, ldy, dtype=x.dtype, device=x.device)
+    else:
+        if y.shape != (rows, store.d_out) or y.dtype != x.dtype:
+            raise ValueError(f"y must be [{rows}, {store.d_out}] of x's dtype")
+        _same_device(index, y=y)
+        ldy = _ld(y, "y")
     if ws is None:
-        nb = lora_w4_workspace_bytes(store, x.dtype, T, k, weighted)
-        ws = torch.empty(nb, dtype=torch.uint8, device=x.device) if nb else None
-    return ws
+        key = (dt, T, k, weights is not None)
+        nb = store._ws_bytes.get(key)
+        if nb is None:
+            if len(store._ws_bytes) >= 1024:
+                store._ws_bytes.clear()
+            nb = store._ws_bytes[key] = lora_w4_workspace_bytes(store, x.dtype, T, k, weights is not None)
+        if nb:
+            ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        ws_ptr = ws.data_ptr() if nb else None
+    else:
+        _same_device(index, ws=ws)
+        nb = ws.numel() * ws.element_size()
+        ws_ptr = _p(ws)
+    _call(name, index, store._ref, dt, _p(x), ldx, *middle[0], _p(y), ldy, T, *middle[1], ws_ptr, nb)
+    return y
 
 
 def lora_w4_apply(store: W4Store, x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
                   ws: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[t] = W x[t] (overwrites y; allocated when None): the 4-bit base layer
     of a store of one matrix, x [T, d_in] bfloat16 or float32."""
-    dt, ldx = _dtype(x, "x"), _ld(x, "x")
-    if x.shape[1] != store.d_in:
-        raise ValueError("x must be [T, d_in]")
     T = x.shape[0]
-    y = _w4_out(y, T, store, x)
-    _on(store.codes.device, x=x, y=y, ws=ws)
-    ws = _w4_ws(store, x, T, 0, False, ws)
-    with _Device(x.device.index):
-        L.check("lora_w4_apply", L.lib().lora_w4_apply(
-            store.ref(), dt, _p(x), ldx, _p(y), _ld(y, "y"), T, _p(ws), ws.numel() if ws is not None else 0, _stream(x)))
-    return y
+    return _w4_run("lora_w4_apply", store, x, T, y, T, 0, None, None, ws, ((), ()))
 
 
 def lora_w4_apply_experts(store: W4Store, x: torch.Tensor, ids: torch.Tensor, weights: Optional[torch.Tensor] = None,
@@ -768,20 +777,17 @@ def lora_w4_apply_experts(store: W4Store, x: torch.Tensor, ids: torch.Tensor, we
     if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 [T, k]")
     T, k = ids.shape
-    dt, ldx = _dtype(x, "x"), _ld(x, "x")
-    if x.shape[1] != store.d_in or x.shape[0] not in (T, T * k):
+    x_rows = x.shape[0]
+    if x_rows != T and x_rows != T * k:
         raise ValueError("x must be [T, d_in] or [T k, d_in]")
-    if weights is not None and (weights.shape != (T, k) or weights.dtype != torch.float32
-                                or not weights.is_contiguous()):
-        raise ValueError("weights must be a contiguous float32 [T, k]")
-    y = _w4_out(y, T if weights is not None else T * k, store, x)
-    _on(store.codes.device, x=x, ids=ids, weights=weights, y=y, ws=ws)
-    ws = _w4_ws(store, x, T, k, weights is not None, ws)
-    with _Device(x.device.index):
-        L.check("lora_w4_apply_experts", L.lib().lora_w4_apply_experts(
-            store.ref(), dt, _p(x), ldx, int(x.shape[0] != T), _p(y), _ld(y, "y"), T, k, _p(ids), _p(weights),
-            _p(ws), ws.numel() if ws is not None else 0, _stream(x)))
-    return y
+    if ids.get_device() != store.device_index:
+        _same_device(store.device_index, ids=ids)
+    if weights is not None:
+        if weights.shape != ids.shape or weights.dtype != torch.float32 or not weights.is_contiguous():
+            raise ValueError("weights must be a contiguous float32 [T, k]")
+        _same_device(store.device_index, weights=weights)
+    return _w4_run("lora_w4_apply_experts", store, x, T * k if weights is None else T, y, T, k, ids, weights, ws,
+                   ((int(x_rows != T),), (k, _p(ids), _p(weights))))
 
 
 _SCORES = {"softmax": L.LORA_ROUTE_SOFTMAX, "sigmoid": L.LORA_ROUTE_SIGMOID}
@@ -796,24 +802,28 @@ def lora_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Op
     runs of experts.  Where fewer than k can be chosen: id -1, weight 0."""
     dt, ldl = _dtype(logits, "logits"), _ld(logits, "logits")
     T, E = logits.shape
-    if score not in _SCORES:
+    mode = _SCORES.get(score)
+    if mode is None:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
-    if bias is not None and (bias.shape != (E,) or bias.dtype != torch.float32 or not bias.is_contiguous()):
-        raise ValueError("bias must be a contiguous float32 [E]")
-    k = int(k)
+    k, index = int(k), logits.get_device()
     if k < 1:
         raise ValueError("k must be positive")
-    if ids is None:
-        ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
-    if weights is None:
-        weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
-    if ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous():
-        raise ValueError("ids must be a contiguous int32 [T, k]")
-    if weights.shape != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
-        raise ValueError("weights must be a contiguous float32 [T, k]")
-    _on(logits.device, bias=bias, ids=ids, weights=weights)
-    with _Device(logits.device.index):
-        L.check("lora_route", L.lib().lora_route(
-            _p(logits), ldl, dt, T, E, k, _SCORES[score], _p(bias), int(groups), int(top_groups), int(renormalize),
-            float(scale), _p(ids), _p(weights), _stream(logits)))
+    if bias is not None:
+        if bias.shape != (E,) or bias.dtype != torch.float32 or not bias.is_contiguous():
+            raise ValueError("bias must be a contiguous float32 [E]")
+        _same_device(index, bias=bias)
+    if index < 0:
+        _same_device(index)
+    outs = []
+    for t, dtype, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
+        if t is None:
+            t = torch.empty(T, k, dtype=dtype, device=logits.device)
+        elif t.shape != (T, k) or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} [T, k]")
+        elif t.get_device() != index:
+            _same_device(index, **{name: t})
+        outs.append(t)
+    ids, weights = outs
+    _call("lora_route", index, _p(logits), ldl, dt, T, E, k, mode, _p(bias), int(groups), int(top_groups),
+          int(renormalize), float(scale), _p(ids), _p(weights))
     return ids, weights

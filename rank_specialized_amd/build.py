@@ -24,7 +24,7 @@ REF_SOURCES = ["stream_ref.hip"]
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = os.environ.get("LORA_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["api.hip", "pack.hip", "segment.hip", "group.hip", "shrink.hip", "expand.hip", "decode.hip", "jd.hip", "rsvd.hip", "multi.hip", "fused.hip", "w4_pack.hip", "w4_rows.hip", "w4_few.hip", "w4_gemm.hip", "w4_api.hip", "route.hip", "validate.cpp", "ranks.cpp"]
+SOURCES = ["api.hip", "pack.hip", "segment.hip", "group.hip", "shrink.hip", "expand.hip", "decode.hip", "jd.hip", "rsvd.hip", "multi.hip", "fused.hip", "w4_pack.hip", "w4_rows_bf16.hip", "w4_rows_f32.hip", "w4_gemm.hip", "w4_run.hip", "w4_api.hip", "route.hip", "validate.cpp", "ranks.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
           f"-I{os.path.join(ROOT, 'include')}", f"-I{CSRC}"]

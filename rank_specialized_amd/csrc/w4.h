@@ -16,16 +16,16 @@ namespace lora {
 // addresses, and a lane's dword is exactly its operand of one 16 x 16 x 32
 // product.  Inside a dword, input 2 i of the eight is nibble i of the low
 // half and input 2 i + 1 nibble i of the high half, and the dword is rotated
-// left by 3: nibble 0 then sits on bits 3..6 of each half, where "or" with
-// 16.0 (bf16, step 1/8) or 128.0 (f16, step 1/8) makes the number 16 + q or
-// 128 + q.
+// left by 2: nibble 0 then sits on bits 2..5 of each half, where "or" with
+// 32.0 in bf16 or 256.0 in f16 (both of step 1/4) makes the number 32 + q or
+// 256 + q, and nibble 1 on bits 6..9, where 16.0 in f16 (step 1/64) makes 16 + q.
 constexpr int kW4Rows = 16;
 constexpr int kW4K = 128;
 constexpr int kW4TileBytes = kW4Rows * kW4K / 2;
 
 // How a group's scale and zero point are held: bf16 scales without zero
-// points in 2 bytes, with them in 4 (the zero point as the bf16 of 16 + z),
-// float32 scales in 8 (scale, 16 + z).
+// points in 2 bytes, with them in 4 (the zero point as the bf16 of 32 + z),
+// float32 scales in 8 (scale, 32 + z).
 enum W4Param { kW4Bf16 = 0, kW4Bf16Zero = 1, kW4F32 = 2 };
 inline int w4_param_kind(int scale_dtype, int has_zeros) {
   return scale_dtype == LORA_DTYPE_F32 ? kW4F32 : (has_zeros ? kW4Bf16Zero : kW4Bf16);
@@ -47,33 +47,35 @@ inline int64_t w4_params_bytes(int n, int d_in, int d_out, int kind, int sub) {
   return n * w4_tiles(d_in, d_out) * w4_tile_param_bytes(kind, sub);
 }
 
-// The few-rows kernel holds its rows of x in LDS: per row k_tiles * 128 values
-// as bf16, of float32 rows three such planes, and 16 bytes more, so that 16
-// rows' pieces of one matrix-core step lie on all banks.  64 KiB, so that two
-// workgroups fit a compute unit.
-constexpr int kW4FewLds = 64 * 1024;
-inline int w4_few_row_bytes(int dtype, int d_in) {
-  return (dtype == LORA_DTYPE_BF16 ? 1 : 3) * w4_k_tiles(d_in) * kW4K * 2 + 16;
-}
-inline int w4_few_rows(int dtype, int d_in) { return kW4FewLds / w4_few_row_bytes(dtype, d_in); }
+// The few-rows kernel holds its rows of x in LDS: per row and 128-input tile
+// 256 bytes (float32 rows: three bf16 planes), and 16 bytes more per row, so
+// that 16 rows' pieces of one matrix-core step lie on all banks.
+inline int w4_lds_row_bytes(int dtype, int tiles) { return (dtype == LORA_DTYPE_BF16 ? 1 : 3) * tiles * kW4K * 2 + 16; }
 
 // How a call is run, and the workspace it takes.
 struct W4Plan {
-  bool sum_in_kernel;  // weighted rows: each token's matrices run through by one workgroup, no partial rows
-  int bm;              // rows per tile of the many-rows kernel; 0: a few-rows kernel
-  size_t part;         // float32 rows [R][d_out] of a weighted call that keeps them
-  size_t xs, up;       // many rows: x as f16, the rows' powers of two
+  int bm;              // rows per tile of the many-rows kernel; 0: the few-rows kernel
+  bool sum_in_kernel;  // few rows, weighted: each token's matrices run through by one workgroup
+  bool keep_parts;     // float32 rows [splits][R][d_out] are kept and summed by a last kernel
+  int rt, nt;          // few rows: 16-output blocks and 16-row blocks of a workgroup
+  int row_cap;         // rows held in LDS at a time
+  bool chunked;        // few rows: not all inputs of the rows in LDS at once
+  int splits, per_split;  // splits of the inputs, tiles of one
+  size_t part;
+  size_t xs, up;             // many rows: x as f16, the rows' powers of two
   size_t hist, perm, tiles;  // many rows by matrix: counts and the number of tiles, the order, the tiles
   size_t ws_bytes;
 };
 // Rows of a weighted call up to which a token's k products are one
-// workgroup's sum (if its rows fit LDS).
+// workgroup's sum (if its rows fit LDS).  8 experts of 1408 -> 2048 for one
+// token: 10.4 us in one kernel, 7.5 + 3.9 us as partial rows and their sum;
+// the partial rows read a matrix once for all its tokens, though, so more
+// than a few tokens are better off with them.
 constexpr int kW4SumRows = 32;
 // Rows per tile of the many-rows kernel.  Larger tiles unpack a code for more
-// rows; 128 rows no longer fit the registers.  Measured (64, 96, 112, 128
-// rows): 8192 rows, 4096 -> 14336: 1089, 936, 1015, 1180 us; 32 experts of
-// 512 rows, 2048 -> 2816: 284, 264, 292, 372 us; 64 experts of 256 rows, 1408
-// -> 2048: 200, 207, 211, 283 us.
+// rows; 112 rows take every register there is.  Measured (64, 96, 112 rows):
+// 8192 rows, 4096 -> 14336: 1076, 905, 965 us; 32 experts of 512 rows, 2048 ->
+// 2816: 291, 272, 273 us; 64 experts of 256 rows, 1408 -> 2048: 202, 207, 221 us.
 constexpr int kW4BigTile = 96, kW4SmallTile = 64;
 constexpr int kW4BigRows = 384;  // rows per matrix from which the big tile is taken
 // Tiles of at most bm rows that R rows of n matrices (and of none) cut into.
@@ -82,18 +84,76 @@ inline int64_t w4_max_tiles(int R, int n, int bm) { return plan_max_runs(R, n + 
 inline W4Plan w4_plan_call(const lora_w4_store& s, int dtype, int T, int k, bool weighted) {
   W4Plan p{};
   if (T <= 0) return p;
-  const int64_t R = (int64_t)T * (k > 0 ? k : 1);
-  p.sum_in_kernel = weighted && R <= kW4SumRows && k <= w4_few_rows(dtype, s.d_in);
-  const int64_t per = (R + s.n - 1) / s.n;  // rows per matrix, on average
-  const int64_t xs_bytes = R * w4_k_tiles(s.d_in) * kW4K * 2;  // 32-bit offsets
-  if (dtype == LORA_DTYPE_BF16 && !p.sum_in_kernel && per > 32 && xs_bytes < ((int64_t)1 << 32)) 
-    p.bm = per >= kW4BigRows ? kW4BigTile : kW4SmallTile;
+  const int R = T * (k > 0 ? k : 1), kt = w4_k_tiles(s.d_in), row_tiles = w4_row_tiles(s.d_out);
+  const bool bf16 = dtype == LORA_DTYPE_BF16, by_row = k > 0 && R <= s.n;
+  const int per = (R + s.n - 1) / s.n;  // rows per matrix, on average
+  p.splits = 1;
+  p.per_split = kt;
+  // The many-rows kernel: rows enough per matrix for its tiles, and tiles
+  // enough for the GPU.  It has x rewritten first and, by matrix, the rows
+  // sorted (5 to 20 us).  Few-rows against many-rows, all kernels: 32 experts
+  // of 12 rows 32 against 48 us, of 32 rows 116 against 88, of 64 rows 150
+  // against 95 (2048 -> 2816); 3584 -> 3584: 128 rows 21 against 34 us, 512
+  // rows 41 against 55; 256 rows of 3584 -> 18944 160 against 69.
+  // Its offsets are 32-bit: the rewritten x and a matrix stay below 2^32 bytes.
+  const int64_t xs_bytes = (int64_t)R * kt * kW4K * 2, matrix_bytes = w4_tiles(s.d_in, s.d_out) * kW4TileBytes;
+  const int bm = per >= kW4BigRows ? kW4BigTile : kW4SmallTile;
+  const int64_t tiles = (k > 0 ? (int64_t)s.n * ((per + bm - 1) / bm) : (R + bm - 1) / bm) * ((s.d_out + 255) / 256);
+  const bool many = k > 0 ? per > 24 : per > 128 && (tiles >= 128 || R >= 768);
+  if (weighted && R <= kW4SumRows && (int64_t)k * w4_lds_row_bytes(dtype, kt) <= 64 * 1024) {
+    p.sum_in_kernel = true;
+    p.row_cap = k;
+  } else if (bf16 && many && xs_bytes < ((int64_t)1 << 32) && matrix_bytes < ((int64_t)1 << 31)) {
+    p.bm = bm;
+    // Tiles too few for the GPU (one or two to a compute unit): their inputs
+    // are split, four tiles of inputs at least to a split.
+    int64_t want = tiles >= 192 ? 1 : (384 + tiles - 1) / tiles;
+    if (want > kt / 4) want = kt / 4;
+    if (want > 1) {
+      p.per_split = (int)((kt + want - 1) / want);
+      p.splits = (kt + p.per_split - 1) / p.per_split;
+    }
+  } else {
+    // A matrix's rows, with room for more than the average.
+    const int rows = k > 0 ? (by_row ? (R < 4 ? R : 4) : per + 3) : R;
+    const int64_t blocks = (int64_t)row_tiles * (by_row ? R : (k > 0 ? (R < s.n ? R : s.n) : 1));
+    p.nt = rows <= 16 ? 1 : (rows <= 32 || !bf16 ? 2 : 4);
+    p.row_cap = rows < 16 * p.nt ? rows : 16 * p.nt;
+    const int64_t all = (int64_t)p.row_cap * w4_lds_row_bytes(dtype, kt);
+    // All inputs of the rows in LDS, where that leaves room for two
+    // workgroups on a compute unit, or there is no more than one for it: 16
+    // rows 3584 -> 3584 6.6 us so, 7.1 + 2.8 (and a sum) in chunks and
+    // splits; but 3584 -> 18944 31 against 13 + 3.9.
+    if (p.nt == 1 && (all <= 64 * 1024 || (blocks < 512 && all <= 128 * 1024))) {
+      // 16-output blocks per workgroup: more share a row's LDS reads, fewer
+      // give every compute unit work.  Waves and tiles in flight go with it
+      // (launch_mode).  One token (blocks): 3584 -> 512 (32) 3.5, 5.4, 8.8 us
+      // with 1, 2, 4; 3584 -> 18944 (1184) 10.0, 11.1, 13.4; eight experts of
+      // 2048 -> 2816 (1408) 10.6, 7.8, 10.2; 40 (7040) 43, 36, 27.
+      p.rt = blocks < 512 ? 0 : (blocks < 1280 ? 1 : (blocks < 2816 ? 2 : 4));
+    } else {
+      // In chunks, and the inputs split until there are about 768 workgroups
+      // of at least eight tiles of inputs: 23 rows 18944 -> 3584 16.2 us with
+      // 13 splits, 22 with 5.
+      p.chunked = true;
+      p.rt = p.nt == 4 ? 2 : 4;
+      const int64_t groups = (blocks + p.rt - 1) / p.rt * (k > 0 ? 1 : (R + p.row_cap - 1) / p.row_cap);
+      int64_t want = (768 + groups - 1) / groups;
+      if (want > kt / 8) want = kt / 8;
+      if (want > 1) {
+        p.per_split = (int)((kt + want - 1) / want);
+        p.per_split = (p.per_split + 3) / 4 * 4;
+        p.splits = (kt + p.per_split - 1) / p.per_split;
+      }
+    }
+  }
   auto take = [&](size_t bytes) {
     const size_t at = p.ws_bytes;
     p.ws_bytes += align_up(bytes, 256);
     return at;
   };
-  if (weighted && !p.sum_in_kernel) p.part = take((size_t)R * (size_t)s.d_out * 4);
+  p.keep_parts = (weighted && !p.sum_in_kernel) || p.splits > 1;
+  if (p.keep_parts) p.part = take((size_t)p.splits * (size_t)R * (size_t)s.d_out * 4);
   if (p.bm > 0) {
     p.xs = take((size_t)xs_bytes);  // R rows where each choice has its own
     p.up = take((size_t)R * 4);
@@ -101,7 +161,7 @@ inline W4Plan w4_plan_call(const lora_w4_store& s, int dtype, int T, int k, bool
       const int64_t chunks = (R + 8191) / 8192;
       p.hist = take(((size_t)chunks * (size_t)(s.n + 1) + 1) * 4);
       p.perm = take((size_t)R * 4);
-      p.tiles = take((size_t)w4_max_tiles((int)R, s.n, p.bm) * 16);
+      p.tiles = take((size_t)w4_max_tiles(R, s.n, p.bm) * 16);
     }
   }
   return p;

@@ -7,9 +7,11 @@
 // unpacked once per 16 NT rows; the waves share the rows of x in LDS, staged
 // 128 inputs at a time by loads that write LDS directly, two buffers.
 //
-// The codes enter the products as f16 numbers: 128 + q is one "and-or" per
-// two codes, and one packed addition takes 128 + z off, leaving q - z itself,
-// exactly (f16 arithmetic is packed, bf16's is not).  x must then be f16 too:
+// The codes enter the products as f16 numbers: 256 + q or 16 + q (the two
+// places of a code in f16's ten fraction bits, so that one shift serves four
+// codes) is one "and-or" per two codes, and one packed addition takes 256 + z
+// or 16 + z off, leaving q - z itself, exactly (f16 arithmetic is packed,
+// bf16's is not).  x must then be f16 too:
 // a first kernel writes each row times the power of two that brings its
 // largest value to [2^14, 2^15), which keeps all eight bits of every bf16
 // value down to 2^-31 of the row's largest (below, the rounding is at most
@@ -180,6 +182,7 @@ struct W4GemmArgs {
   const int4* tiles;
   const int32_t* n_tiles;
   int tiles_o, tiles_t;
+  int per_split;  // tiles of inputs per split (blockIdx.y): float32 rows [splits][R]
 };
 
 constexpr int kWaves = 4, kRT = 4;  // waves; blocks of 16 outputs per wave
@@ -224,6 +227,7 @@ __device__ __forceinline__ void gemm_step(const char* __restrict__ rd, char* __r
   if (more)
 #pragma unroll
     for (int q = 0; q < NT; ++q) dma16(xr, wr + q * 1024 * kWaves, src[q], soff);
+  __builtin_amdgcn_s_setprio(1);  // a wave with products ahead goes before one that unpacks
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     uint4 x[4];
@@ -243,6 +247,7 @@ __device__ __forceinline__ void gemm_step(const char* __restrict__ rd, char* __r
         for (int v = 0; v < 4; ++v) acc[t][a][v] = fmaf(sc[a][s], c[a][v], acc[t][a][v]);
     }
   }
+  __builtin_amdgcn_s_setprio(0);
 }
 
 template <int KIND, int SUB, int NT, bool F32OUT>
@@ -264,13 +269,12 @@ void w4_gemm_kernel(const W4GemmArgs p) {
     m = t.z;
   }
   const int o0 = to * kCols;
-  if (e >= p.n) {  // rows without a matrix: empty sums
+  if (e >= p.n) {  // rows without a matrix: empty sums (float32 rows are then not read)
+    if (F32OUT) return;
     for (int i = tid; i < m * (kCols / 8); i += 64 * kWaves) {
       const int r = p.perm[pos0 + i / (kCols / 8)], o = o0 + 8 * (i % (kCols / 8));
       if (o >= p.d_out) continue;
-      char* at = p.y + (int64_t)r * p.ldy_bytes + (int64_t)o * (F32OUT ? 4 : 2);
-      st16(at, make_uint4(0, 0, 0, 0));
-      if (F32OUT) st16(at + 16, make_uint4(0, 0, 0, 0));
+      st16(p.y + (int64_t)r * p.ldy_bytes + 2 * (int64_t)o, make_uint4(0, 0, 0, 0));
     }
     return;
   }
@@ -292,25 +296,26 @@ void w4_gemm_kernel(const W4GemmArgs p) {
   const uint32_t lane_row = col * kW4K * 2;
 
   // ---- codes: one tile of each of the wave's four output blocks, loaded a
-  // step ahead
+  // step ahead.  A matrix's codes are below 2^32 bytes (w4_plan_call).
   uint4 code[kRT];
   W4Params<KIND, SUB> par[kRT];
-  const char *cb[kRT], *pb[kRT];
+  constexpr int kParBytes = kW4Rows * W4Params<KIND, SUB>::kBytes;  // of a tile
+  const rsrc_t cr = make_rsrc(p.codes + e * p.code_stride, (uint32_t)p.code_stride);
+  const rsrc_t pr = make_rsrc(p.params + e * p.param_stride, (uint32_t)p.param_stride);
+  uint32_t tile0[kRT];
 #pragma unroll
-  for (int a = 0; a < kRT; ++a) {
-    const int64_t t = (int64_t)min(to * (kCols / 16) + kRT * w + a, p.row_tiles - 1) * p.k_tiles;
-    cb[a] = p.codes + e * p.code_stride + t * kW4TileBytes;
-    pb[a] = p.params + e * p.param_stride + t * kW4Rows * W4Params<KIND, SUB>::kBytes;
-  }
+  for (int a = 0; a < kRT; ++a)
+    tile0[a] = (uint32_t)min(to * (kCols / 16) + kRT * w + a, p.row_tiles - 1) * (uint32_t)p.k_tiles;
   const uint32_t lane16 = 16 * lane, lane_par = col * W4Params<KIND, SUB>::kBytes;
   auto fetch = [&](int kt) {
 #pragma unroll
     for (int a = 0; a < kRT; ++a) {
-      code[a] = ld16(cb[a] + (int64_t)kt * kW4TileBytes + lane16);
-      par[a].load(pb[a] + (int64_t)kt * (kW4Rows * W4Params<KIND, SUB>::kBytes) + lane_par);
+      code[a] = buf_ld16(cr, lane16, (tile0[a] + kt) * kW4TileBytes);
+      par[a].load(pr, lane_par, (tile0[a] + kt) * kParBytes);
     }
   };
-  const uint32_t mask = w4_scalar(kCodeMask), magic = w4_vector(kMagicF16);
+  const uint32_t mask_a = w4_scalar(kCodeMask), mask_b = w4_scalar(kCodeMask << 4);
+  const uint32_t magic_a = w4_vector(kMagicF16A), magic_b = w4_vector(kMagicF16B);
 
   f32x4_t acc[NT][kRT];
 #pragma unroll
@@ -318,11 +323,12 @@ void w4_gemm_kernel(const W4GemmArgs p) {
 #pragma unroll
     for (int a = 0; a < kRT; ++a) acc[t][a] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+  const int k0 = (int)blockIdx.y * p.per_split, k1 = min(p.k_tiles, k0 + p.per_split);
 #pragma unroll
-  for (int q = 0; q < NT; ++q) dma16(xr, fill + q * 1024 * kWaves, src[q], 0);
-  fetch(0);
-  for (int kt = 0; kt < p.k_tiles; ++kt) {
-    const bool more = kt + 1 < p.k_tiles;
+  for (int q = 0; q < NT; ++q) dma16(xr, fill + q * 1024 * kWaves, src[q], (uint32_t)k0 * kW4K * 2);
+  fetch(k0);
+  for (int kt = k0; kt < k1; ++kt) {
+    const bool more = kt + 1 < k1;
     // This step's x and codes were asked for a whole step ago; every wave has
     // finished with the buffer that is filled next.
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -336,20 +342,22 @@ void w4_gemm_kernel(const W4GemmArgs p) {
 #pragma unroll
       for (int s = 0; s < SUB; ++s) {
         sc[a][s] = par[a].scale(s);
-        const _Float16 z = (_Float16)(-112.f - par[a].zero16(s));  // -(128 + z)
-        const f16x2_t zz = {z, z};
+        const float z32 = par[a].zero32(s);
+        const _Float16 za = (_Float16)(-224.f - z32), zb = (_Float16)(16.f - z32);  // -(256 + z), -(16 + z)
+        const f16x2_t zza = {za, za}, zzb = {zb, zb};
+        auto sum = [](uint32_t v, f16x2_t z) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, v) + z); };
 #pragma unroll
         for (int j = s * (4 / SUB); j < (s + 1) * (4 / SUB); ++j) {
-          const uint4 v = w4_expand(cw[j], mask, magic);
-          b[a][j] = make_uint4(__builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, v.x) + zz),
-                               __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, v.y) + zz),
-                               __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, v.z) + zz),
-                               __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2_t, v.w) + zz));
+          const uint32_t lo = cw[j], hi = __builtin_amdgcn_alignbit(lo, lo, 8);
+          b[a][j] = make_uint4(sum((lo & mask_a) | magic_a, zza), sum((lo & mask_b) | magic_b, zzb),
+                               sum((hi & mask_a) | magic_a, zza), sum((hi & mask_b) | magic_b, zzb));
         }
       }
     }
-    if (more) fetch(kt + 1);
-    const int cur = kt & 1;
+    // Past the last tile its codes are read again: without a branch the loads
+    // go straight into the registers that have just been read.
+    fetch(more ? kt + 1 : kt);
+    const int cur = (kt - k0) & 1;
     gemm_step<KIND, SUB, NT>(lds + cur * stage_bytes<NT>(), fill + (cur ^ 1) * stage_bytes<NT>(), more, xr, src,
                              (uint32_t)(kt + 1) * kW4K * 2, b, sc, lane_row, h, col, acc);
   }
@@ -365,7 +373,7 @@ void w4_gemm_kernel(const W4GemmArgs p) {
         if (row >= m) continue;
         const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos0 + row] : (uint32_t)(pos0 + row);
         const float u = p.up[r / (uint32_t)p.x_div];
-        float* yrow = reinterpret_cast<float*>(p.y + (int64_t)r * p.ldy_bytes);
+        float* yrow = reinterpret_cast<float*>(p.y + ((int64_t)blockIdx.y * p.R + r) * p.ldy_bytes);
 #pragma unroll
         for (int a = 0; a < kRT; ++a) {
           const int o = o0 + 16 * (kRT * w + a) + col;
@@ -408,8 +416,9 @@ template <int KIND, int SUB, int NT>
 hipError_t launch_nt(const W4GemmArgs& a, bool f32_out, hipStream_t stream) {
   const int64_t grid = (int64_t)a.tiles_o * a.tiles_t;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  if (f32_out) hipLaunchKernelGGL((w4_gemm_kernel<KIND, SUB, NT, true>), dim3((unsigned)grid), dim3(64 * kWaves), 0, stream, a);
-  else hipLaunchKernelGGL((w4_gemm_kernel<KIND, SUB, NT, false>), dim3((unsigned)grid), dim3(64 * kWaves), 0, stream, a);
+  const unsigned splits = (unsigned)((a.k_tiles + a.per_split - 1) / a.per_split);
+  if (f32_out) hipLaunchKernelGGL((w4_gemm_kernel<KIND, SUB, NT, true>), dim3((unsigned)grid, splits), dim3(64 * kWaves), 0, stream, a);
+  else hipLaunchKernelGGL((w4_gemm_kernel<KIND, SUB, NT, false>), dim3((unsigned)grid, splits), dim3(64 * kWaves), 0, stream, a);
   return hipGetLastError();
 }
 template <int KIND, int SUB>
@@ -435,6 +444,7 @@ hipError_t launch_w4_gemm(const W4Call& c, hipStream_t stream) {
   a.d_out = s.d_out;
   a.x_div = c.x_div;
   a.R = c.R;
+  a.per_split = pl.per_split;
   a.xs = c.ws + pl.xs;
   a.up = reinterpret_cast<const float*>(c.ws + pl.up);
   const int x_rows = c.R / c.x_div;
@@ -465,7 +475,7 @@ hipError_t launch_w4_gemm(const W4Call& c, hipStream_t stream) {
     a.n_tiles = g.n_tiles;
     a.tiles_t = (int)w4_max_tiles(c.R, s.n, pl.bm);
   }
-  const bool f32_out = c.weights != nullptr;
+  const bool f32_out = pl.keep_parts;
   a.y = f32_out ? c.ws + pl.part : reinterpret_cast<char*>(c.y);
   a.ldy_bytes = f32_out ? (int64_t)s.d_out * 4 : c.ldy * 2;
   switch (kind * 8 + sub) {

@@ -29,11 +29,9 @@ struct W4Call {
   char* ws;
 };
 hipError_t launch_w4(const W4Call& c, hipStream_t stream);
-hipError_t launch_w4_rows(const W4Call& c, hipStream_t stream);
+hipError_t launch_w4_rows_bf16(const W4Call& c, hipStream_t stream);
+hipError_t launch_w4_rows_f32(const W4Call& c, hipStream_t stream);
 hipError_t launch_w4_gemm(const W4Call& c, hipStream_t stream);
-struct W4RowsArgs;
-hipError_t launch_w4_few(const W4RowsArgs& a, int dtype, int kind, int sub, unsigned gy, hipStream_t stream);
-hipError_t launch_w4_combine(const W4Call& c, const float* part, hipStream_t stream);
 
 struct RouteArgs {
   const void* logits;

@@ -6,9 +6,9 @@
 namespace lora {
 
 // Four operand dwords (two numbers each) of a lane's eight codes: each half
-// of `magic` is 16.0 in bf16 (0x4180) or 128.0 in f16 (0x5800), whose last
-// bits the code takes: 16 + q, 128 + q, exact.  `mask` and `magic` come from
-// w4_scalar and w4_vector, so that each step is one v_and_or_b32.
+// of `magic` is 32.0 in bf16 (0x4200), whose last bits the code takes: 32 + q,
+// exact.  `mask` and `magic` come from w4_scalar and w4_vector, so that each
+// step is one v_and_or_b32.
 __device__ __forceinline__ uint4 w4_expand(uint32_t w, uint32_t mask, uint32_t magic) {
   return make_uint4((w & mask) | magic, ((w >> 4) & mask) | magic, ((w >> 8) & mask) | magic,
                     (__builtin_amdgcn_alignbit(w, w, 12) & mask) | magic);
@@ -28,23 +28,24 @@ __device__ __forceinline__ uint32_t w4_vector(uint32_t v) {
   asm("v_mov_b32 %0, %1" : "=v"(r) : "s"(w4_scalar(v)));
   return r;
 }
-constexpr uint32_t kCodeMask = 0x00780078u;
+constexpr uint32_t kCodeMask = 0x003c003cu;
 // q - z itself, exact in bf16 (at most five bits): the eight numbers widened,
-// 16 + z taken off, the halves put together again (27 instructions for eight
+// 32 + z taken off, the halves put together again (27 instructions for eight
 // codes against 7).
-__device__ __forceinline__ uint4 w4_expand_exact(uint32_t w, uint32_t mask, uint32_t magic, float zero16) {
+__device__ __forceinline__ uint4 w4_expand_exact(uint32_t w, uint32_t mask, uint32_t magic, float zero32) {
   const uint4 v = w4_expand(w, mask, magic);
   const uint32_t in[4] = {v.x, v.y, v.z, v.w};
   uint32_t out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = bf16_lo(in[i]) - zero16, hi = bf16_hi(in[i]) - zero16;
+    const float lo = bf16_lo(in[i]) - zero32, hi = bf16_hi(in[i]) - zero32;
     out[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
   }
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
-constexpr uint32_t kMagicBf16 = 0x41804180u;
-constexpr uint32_t kMagicF16 = 0x58005800u;
+constexpr uint32_t kMagicBf16 = 0x42004200u;
+// f16: a code on bits 2..5 of 256 (step 1/4), on bits 6..9 of 16 (step 1/64)
+constexpr uint32_t kMagicF16A = 0x5c005c00u, kMagicF16B = 0x4c004c00u;
 
 // A lane's scales and zero points of one tile: SUB groups of its output row.
 template <int KIND, int SUB>
@@ -68,14 +69,30 @@ struct W4Params {
       }
     }
   }
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t voff, uint32_t soff) {
+    if constexpr (kBytes == 2) {
+      w[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+    } else if constexpr (kBytes == 4) {
+      w[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+    } else if constexpr (kBytes == 8) {
+      const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0));
+      w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 v = buf_ld16(r, voff + 16 * i, soff);
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+    }
+  }
   __device__ __forceinline__ float scale(int s) const {
     if constexpr (KIND == kW4Bf16) return (s & 1) ? bf16_hi(w[s >> 1]) : bf16_lo(w[s >> 1]);
     else if constexpr (KIND == kW4Bf16Zero) return bf16_lo(w[s]);
     else return __uint_as_float(w[2 * s]);
   }
-  // 16 + z
-  __device__ __forceinline__ float zero16(int s) const {
-    if constexpr (KIND == kW4Bf16) return 24.f;
+  // 32 + z
+  __device__ __forceinline__ float zero32(int s) const {
+    if constexpr (KIND == kW4Bf16) return 40.f;
     else if constexpr (KIND == kW4Bf16Zero) return bf16_hi(w[s]);
     else return __uint_as_float(w[2 * s + 1]);
   }
@@ -118,70 +135,5 @@ struct XFrag<F32> {
     for (int q = 0; q < 3; ++q) o[q] = make_uint4(out[q][0], out[q][1], out[q][2], out[q][3]);
   }
 };
-
-// What the row kernels are called with.
-struct W4RowsArgs {
-  const char* codes;
-  const char* params;
-  int64_t code_stride, param_stride;  // bytes per matrix
-  int n, k_tiles, row_tiles, d_in, d_out;
-  const char* x;
-  int64_t ldx_bytes;
-  int x_div;
-  char* y;  // rows of the output type, or of float32 (f32_out)
-  int64_t ldy_bytes;
-  int R, k;
-  const int32_t* ids;    // nullptr: matrix 0
-  const float* weights;  // a token's rows summed by one workgroup
-  int by_row;            // routed: blockIdx.y is a row (the first row of its matrix works), else a matrix
-  int f32_out;
-  int row_cap;           // rows that the kernel holds in LDS at a time
-};
-
-constexpr int kListMax = 4096;  // rows of a routed call that are listed at a time
-
-template <typename E>
-__device__ __forceinline__ void w4_store(char* row, int o, float v, int f32_out) {
-  if (E::kBytes == 4 || f32_out) reinterpret_cast<float*>(row)[o] = v;
-  else reinterpret_cast<uint16_t*>(row)[o] = (uint16_t)f32_to_bf16(v);
-}
-
-// The rows of [win, win + kListMax) whose id is e (or, `none`, outside
-// [0, n)), ascending, into `list`; returns their number.  Per chunk of 64 W
-// rows, each wave counts its 64 by ballot and the waves' counts are added up
-// in order.
-template <int W>
-__device__ __forceinline__ int w4_rows_of(const W4RowsArgs& p, int e, bool none, int win, uint16_t* list, int* s_cnt) {
-  const int tid = (int)threadIdx.x, lane = tid & 63, w = tid >> 6;
-  const int end = min(p.R, win + kListMax);
-  int cnt = 0;
-  for (int r0 = win; r0 < end; r0 += 64 * W) {
-    const int r = r0 + tid;
-    const int id = r < end ? p.ids[r] : 0;
-    const bool hit = r < end && (none ? (unsigned)id >= (unsigned)p.n : id == e);
-    const uint64_t mask = __ballot(hit);
-    if (lane == 0) s_cnt[w] = __popcll(mask);
-    __syncthreads();
-    int before = cnt, total = cnt;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      before += i < w ? s_cnt[i] : 0;
-      total += s_cnt[i];
-    }
-    if (hit) list[before + __popcll(mask & lanemask_lt())] = (uint16_t)(r - win);
-    cnt = total;
-    __syncthreads();
-  }
-  return cnt;
-}
-
-// Empty sums: outputs [o0, o0 + width) of `cnt` listed rows.
-template <typename E>
-__device__ __forceinline__ void w4_zero_rows(const W4RowsArgs& p, int win, const uint16_t* list, int cnt, int o0, int width) {
-  for (int i = (int)threadIdx.x; i < cnt * width; i += (int)blockDim.x) {
-    const int o = o0 + i % width;
-    if (o < p.d_out) w4_store<E>(p.y + (int64_t)(win + list[i / width]) * p.ldy_bytes, o, 0.f, p.f32_out);
-  }
-}
 
 }  // namespace lora

@@ -1,6 +1,6 @@
 // Lays a checkpoint's 4-bit codes, scales and zero points out for the 4-bit
 // base products (the layout: w4.h).  Run once when a layer is loaded: it
-// moves bits and computes nothing but 16 + z, so every code, scale and zero
+// moves bits and computes nothing but 32 + z, so every code, scale and zero
 // point is held exactly.
 #include "device_common.h"
 #include "w4_kernels.h"
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const W4PackArgs p) {
       out |= ((v >> (8 * i)) & 15u) << (4 * i);
       out |= ((v >> (8 * i + 4)) & 15u) << (4 * i + 16);
     }
-    w[j] = (out << 3) | (out >> 29);
+    w[j] = (out << 2) | (out >> 30);
   }
   st16(p.codes + tile * kW4TileBytes + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
 
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(const W4PackArgs p) {
     const int g = (kW4K * kt + gran * s) / p.group;
     const bool in = po < p.d_out && kW4K * kt + gran * s < p.d_in;
     const int64_t at = (e * p.d_out + po) * p.groups + g;
-    const float zz = in && p.zeros ? 16.f + (float)(p.zeros[at] & 15) : 24.f;
+    const float zz = in && p.zeros ? 32.f + (float)(p.zeros[at] & 15) : 40.f;
     const int64_t idx = tile * kW4Rows * p.sub + lane;
     if (p.kind == kW4F32) {
       const float sc = in ? reinterpret_cast<const float*>(p.scales)[at] : 0.f;

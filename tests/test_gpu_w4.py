@@ -1,12 +1,12 @@
 """The 4-bit base products on the GPU against the float64 oracle.
 
-Tolerance of a value.  Every product (16 + q) x or (q - z) x is exact in
+Tolerance of a value.  Every product (32 + q) x or (q - z) x is exact in
 float32 (a bf16 value, or a bf16 part of a float32 one, times an integer below
-32).  A product then passes through at most `gran` + 2 additions inside its
+64).  A product then passes through at most `gran` + 2 additions inside its
 group of `gran` <= 128 inputs, one scaling, and the additions of the groups
 and of the waves: gran + groups + 32 roundings in all, each at most 2^-23 of
 the magnitudes added up (a matrix core may truncate).  Those are bounded by
-sum |s| (16 + q + 16 + z) |x| (the products and the correction, in absolute
+sum |s| (32 + q + 32 + z) |x| (the products and the correction, in absolute
 value).  A weighted sum multiplies each of its rows' bounds by the weight and
 adds k + 2 roundings.  y then rounds once: half a step, 2^-8 (bf16) or 2^-24
 (float32) of the value.  The f16 form holds x to 2^-25 of its row's largest
