@@ -814,16 +814,18 @@ def lora_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Op
         _same_device(index, bias=bias)
     if index < 0:
         _same_device(index)
-    outs = []
-    for t, dtype, name in ((ids, torch.int32, "ids"), (weights, torch.float32, "weights")):
-        if t is None:
-            t = torch.empty(T, k, dtype=dtype, device=logits.device)
-        elif t.shape != (T, k) or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} [T, k]")
-        elif t.get_device() != index:
-            _same_device(index, **{name: t})
-        outs.append(t)
-    ids, weights = outs
-    _call("lora_route", index, _p(logits), ldl, dt, T, E, k, mode, _p(bias), int(groups), int(top_groups),
-          int(renormalize), float(scale), _p(ids), _p(weights))
+    if ids is None:
+        ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+    elif ids.shape != (T, k) or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 [T, k]")
+    else:
+        _same_device(index, ids=ids)
+    if weights is None:
+        weights = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+    elif weights.shape != (T, k) or weights.dtype != torch.float32 or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 [T, k]")
+    else:
+        _same_device(index, weights=weights)
+    _call("lora_route", index, _p(logits), ldl, dt, T, E, k, mode, bias.data_ptr() if bias is not None else None,
+          int(groups), int(top_groups), int(renormalize), float(scale), _p(ids), _p(weights))
     return ids, weights

@@ -61,7 +61,10 @@ struct Key64 {
   __device__ bool same(Key64 o) const { return v == o.v; }
   __device__ static Key64 wave_largest(Key64 k) {
     const uint32_t hi = wave_max((uint32_t)(k.v >> 32));
-    const uint32_t lo = wave_max((uint32_t)(k.v >> 32) == hi ? (uint32_t)k.v : 0u);
+    const uint64_t at = __ballot((uint32_t)(k.v >> 32) == hi);
+    // One lane has the largest upper half, nearly always.
+    const uint32_t lo = (at & (at - 1)) == 0 ? (uint32_t)__builtin_amdgcn_readlane((int)k.v, __ffsll((unsigned long long)at) - 1)
+                                             : wave_max((uint32_t)(k.v >> 32) == hi ? (uint32_t)k.v : 0u);
     return {((uint64_t)hi << 32) | lo};
   }
   __device__ double value() const {
@@ -84,6 +87,24 @@ template <typename E>
 __device__ __forceinline__ float logit_at(const void* p, int64_t i) {
   if constexpr (E::kBytes == 2) return bf16_lo(reinterpret_cast<const uint16_t*>(p)[i]);
   else return reinterpret_cast<const float*>(p)[i];
+}
+
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v, int d) { return (uint32_t)__shfl_xor((int)v, d); }
+__device__ __forceinline__ uint64_t lane_xor(uint64_t v, int d) {
+  return ((uint64_t)lane_xor((uint32_t)(v >> 32), d) << 32) | lane_xor((uint32_t)v, d);
+}
+__device__ __forceinline__ uint32_t from_lane(uint32_t v, int l) { return (uint32_t)__shfl((int)v, l); }
+__device__ __forceinline__ uint64_t from_lane(uint64_t v, int l) {
+  return ((uint64_t)from_lane((uint32_t)(v >> 32), l) << 32) | from_lane((uint32_t)v, l);
+}
+
+// A group's score from its largest and second largest key.
+template <typename Key>
+__device__ __forceinline__ Key group_score(Key a, Key b, bool pair) {
+  if constexpr (sizeof(Key) == 8) {
+    if (pair) return a.any() && b.any() ? Key::of(a.value() + b.value()) : Key::none();
+  }
+  return a;
 }
 
 // WIDE: keys are the float64 c; else the logits.
@@ -140,31 +161,55 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs p) {
     // Group g's score on lane g (groups <= 64): its largest key, or the sum
     // of its two largest c.
     const int n = p.E / p.groups;
+    const bool pair = WIDE && !softmax && n > 1;
     Key mine = Key::none();
-    for (int g = 0; g < p.groups; ++g) {
-      Key a = Key::none(), b = Key::none();
+    if (n <= 64 && (n & (n - 1)) == 0) {
+      // A group is n neighbouring lanes of one value, and 64 / n groups are
+      // reduced at once: (largest, second) pairs exchanged across n lanes.
+      const int per = 64 / n;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = 64 * i + lane;
-        if (e >= g * n && e < (g + 1) * n) {
-          if (key[i].above(a)) {
-            b = a;
-            a = key[i];
-          } else if (key[i].above(b)) {
-            b = key[i];
+        Key a = key[i], b = Key::none();
+        for (int d = 1; d < n; d <<= 1) {
+          Key oa, ob;
+          oa.v = lane_xor(a.v, d);
+          if (pair) ob.v = lane_xor(b.v, d);
+          const Key low = a.above(oa) ? oa : a;
+          a = a.above(oa) ? a : oa;
+          if (pair) {
+            b = b.above(ob) ? b : ob;
+            b = b.above(low) ? b : low;
           }
         }
+        Key s = group_score(a, b, pair);
+        s.v = from_lane(s.v, (lane % per) * n);
+        if (lane / per == i) mine = s;
       }
-      Key score = Key::wave_largest(a);
-      if constexpr (WIDE) {
-        if (!softmax && n > 1) {
-          // The second largest: the largest is taken out on one lane.
-          const uint64_t at = __ballot(a.same(score));
-          const Key rest = Key::wave_largest(lane == __ffsll((unsigned long long)at) - 1 ? b : a);
-          score = score.any() && rest.any() ? Key::of(score.value() + rest.value()) : Key::none();
+      if (lane >= p.groups) mine = Key::none();
+    } else {
+      for (int g = 0; g < p.groups; ++g) {
+        Key a = Key::none(), b = Key::none();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int e = 64 * i + lane;
+          if (e >= g * n && e < (g + 1) * n) {
+            if (key[i].above(a)) {
+              b = a;
+              a = key[i];
+            } else if (key[i].above(b)) {
+              b = key[i];
+            }
+          }
         }
+        const Key top = Key::wave_largest(a);
+        Key rest = Key::none();
+        if (pair) {  // the largest is taken out on one lane
+          const uint64_t at = __ballot(a.same(top));
+          rest = Key::wave_largest(lane == __ffsll((unsigned long long)at) - 1 ? b : a);
+        }
+        const Key s = group_score(top, rest, pair);
+        if (lane == g) mine = s;
       }
-      if (lane == g) mine = score;
     }
     // A group's rank: those with a larger score, or the same and a lower index.
     int rank = 0;

@@ -78,6 +78,7 @@ constexpr int kW4SumRows = 32;
 // 2816: 291, 272, 273 us; 64 experts of 256 rows, 1408 -> 2048: 202, 207, 221 us.
 constexpr int kW4BigTile = 96, kW4SmallTile = 64;
 constexpr int kW4BigRows = 384;  // rows per matrix from which the big tile is taken
+constexpr int kW4Chunk = 4096;  // rows sorted by one workgroup
 // Tiles of at most bm rows that R rows of n matrices (and of none) cut into.
 inline int64_t w4_max_tiles(int R, int n, int bm) { return plan_max_runs(R, n + 1, bm); }
 
@@ -158,7 +159,7 @@ inline W4Plan w4_plan_call(const lora_w4_store& s, int dtype, int T, int k, bool
     p.xs = take((size_t)xs_bytes);  // R rows where each choice has its own
     p.up = take((size_t)R * 4);
     if (k > 0) {
-      const int64_t chunks = (R + 8191) / 8192;
+      const int64_t chunks = (R + kW4Chunk - 1) / kW4Chunk;
       p.hist = take(((size_t)chunks * (size_t)(s.n + 1) + 1) * 4);
       p.perm = take((size_t)R * 4);
       p.tiles = take((size_t)w4_max_tiles(R, s.n, p.bm) * 16);

@@ -35,12 +35,48 @@ __device__ __forceinline__ f32x4_t mfma_f16(const uint4& a, const uint4& b, f32x
                                                 0);
 }
 
+struct W4GroupArgs {
+  const int32_t* ids;
+  int R, n, chunks, bm;
+  int32_t* hist;    // [chunks][n + 1]
+  int32_t* perm;    // [R]: rows, ascending matrix
+  int4* tiles;      // matrix (n: none), first position, rows
+  int32_t* n_tiles;
+};
+constexpr int kChunk = kW4Chunk;  // rows counted, and placed, by one workgroup
+
+// Rows per matrix (n: none) of one chunk.
+__device__ __forceinline__ void count_chunk(const W4GroupArgs& g, int chunk) {
+  __shared__ int hist[LORA_W4_MAX_N + 1];
+  const int tid = (int)threadIdx.x, threads = (int)blockDim.x, n1 = g.n + 1;
+  for (int i = tid; i < n1; i += threads) hist[i] = 0;
+  __syncthreads();
+  const int r0 = chunk * kChunk, r1 = min(g.R, r0 + kChunk);
+  constexpr int kAhead = 8;  // ids asked for together
+  for (int r = r0 + tid; r < r1; r += kAhead * threads) {
+    int id[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) id[i] = g.ids[min(r + i * threads, r1 - 1)];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (r + i * threads < r1) atomicAdd(&hist[(unsigned)id[i] < (unsigned)g.n ? id[i] : g.n], 1);
+  }
+  __syncthreads();
+  for (int i = tid; i < n1; i += threads) g.hist[(int64_t)chunk * n1 + i] = hist[i];
+}
+
 // ------------------------------------------------------------ x as f16
 // One wave per row: xs[r] = f16(x[r] 2^-e), zeros up to the last tile's end,
-// and up[r] = 2^e.  A row's infinities and NaNs stay what they are.
+// and up[r] = 2^e.  A row's infinities and NaNs stay what they are.  The
+// first g.chunks workgroups count the rows per matrix instead.
 __global__ __launch_bounds__(256) void w4_f16_kernel(const char* __restrict__ x, int64_t ldx_bytes, int rows, int d_in,
-                                                    int kp, char* __restrict__ xs, float* __restrict__ up) {
-  const int r = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63;
+                                                    int kp, char* __restrict__ xs, float* __restrict__ up,
+                                                    const W4GroupArgs g) {
+  if ((int)blockIdx.x < g.chunks) {
+    count_chunk(g, (int)blockIdx.x);
+    return;
+  }
+  const int r = ((int)blockIdx.x - g.chunks) * 4 + ((int)threadIdx.x >> 6), lane = (int)threadIdx.x & 63;
   if (r >= rows) return;
   const char* src = x + (int64_t)r * ldx_bytes;
   uint32_t top = 0;  // the largest exponent below that of infinity
@@ -80,31 +116,7 @@ __global__ __launch_bounds__(256) void w4_f16_kernel(const char* __restrict__ x,
 }
 
 // ------------------------------------------------------------ rows by matrix
-// Counts per matrix (n: none) of one workgroup's kChunk rows.
-constexpr int kChunk = 8192, kGroupThreads = 1024;
-
-struct W4GroupArgs {
-  const int32_t* ids;
-  int R, n, chunks, bm;
-  int32_t* hist;    // [chunks][n + 1]
-  int32_t* perm;    // [R]: rows, ascending matrix
-  int4* tiles;      // matrix (n: none), first position, rows
-  int32_t* n_tiles;
-};
-
-__global__ __launch_bounds__(kGroupThreads) void w4_count_kernel(const W4GroupArgs p) {
-  __shared__ int hist[LORA_W4_MAX_N + 1];
-  const int tid = (int)threadIdx.x, n1 = p.n + 1;
-  for (int i = tid; i < n1; i += kGroupThreads) hist[i] = 0;
-  __syncthreads();
-  const int r0 = (int)blockIdx.x * kChunk, r1 = min(p.R, r0 + kChunk);
-  for (int r = r0 + tid; r < r1; r += kGroupThreads) {
-    const int id = p.ids[r];
-    atomicAdd(&hist[(unsigned)id < (unsigned)p.n ? id : p.n], 1);
-  }
-  __syncthreads();
-  for (int i = tid; i < n1; i += kGroupThreads) p.hist[(int64_t)blockIdx.x * n1 + i] = hist[i];
-}
+constexpr int kGroupThreads = 1024;
 
 // Each workgroup places its rows: first position of a matrix, plus the rows
 // of earlier workgroups, plus a counter.  (The order of a matrix's rows may
@@ -160,9 +172,13 @@ __global__ __launch_bounds__(kGroupThreads) void w4_place_kernel(const W4GroupAr
   if (blockIdx.x == 0 && tid == 0) *p.n_tiles = all.y + (n1 > kGroupThreads ? extra : 0);
   __syncthreads();
   const int r0 = (int)blockIdx.x * kChunk, r1 = min(p.R, r0 + kChunk);
-  for (int r = r0 + tid; r < r1; r += kGroupThreads) {
-    const int id = p.ids[r];
-    p.perm[atomicAdd(&pos[(unsigned)id < (unsigned)p.n ? id : p.n], 1)] = r;
+  int id[kChunk / kGroupThreads];
+#pragma unroll
+  for (int i = 0; i < kChunk / kGroupThreads; ++i) id[i] = p.ids[min(r0 + tid + i * kGroupThreads, r1 - 1)];
+#pragma unroll
+  for (int i = 0; i < kChunk / kGroupThreads; ++i) {
+    const int r = r0 + tid + i * kGroupThreads;
+    if (r < r1) p.perm[atomicAdd(&pos[(unsigned)id[i] < (unsigned)p.n ? id[i] : p.n], 1)] = r;
   }
 }
 
@@ -448,15 +464,8 @@ hipError_t launch_w4_gemm(const W4Call& c, hipStream_t stream) {
   a.xs = c.ws + pl.xs;
   a.up = reinterpret_cast<const float*>(c.ws + pl.up);
   const int x_rows = c.R / c.x_div;
-  hipLaunchKernelGGL(w4_f16_kernel, dim3((unsigned)((x_rows + 3) / 4)), dim3(256), 0, stream,
-                     reinterpret_cast<const char*>(c.x), c.ldx * 2, x_rows, s.d_in, a.k_tiles * kW4K, c.ws + pl.xs,
-                     reinterpret_cast<float*>(c.ws + pl.up));
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  a.tiles_o = (s.d_out + kCols - 1) / kCols;
-  a.tiles_t = (c.R + pl.bm - 1) / pl.bm;
+  W4GroupArgs g{};
   if (c.ids != nullptr) {
-    W4GroupArgs g{};
     g.ids = c.ids;
     g.R = c.R;
     g.n = s.n;
@@ -465,9 +474,16 @@ hipError_t launch_w4_gemm(const W4Call& c, hipStream_t stream) {
     g.hist = reinterpret_cast<int32_t*>(c.ws + pl.hist);
     g.perm = reinterpret_cast<int32_t*>(c.ws + pl.perm);
     g.tiles = reinterpret_cast<int4*>(c.ws + pl.tiles);
-    g.n_tiles = reinterpret_cast<int32_t*>(c.ws + pl.hist) + (int64_t)g.chunks * (s.n + 1);
-    hipLaunchKernelGGL(w4_count_kernel, dim3((unsigned)g.chunks), dim3(kGroupThreads), 0, stream, g);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    g.n_tiles = g.hist + (int64_t)g.chunks * (s.n + 1);
+  }
+  hipLaunchKernelGGL(w4_f16_kernel, dim3((unsigned)(g.chunks + (x_rows + 3) / 4)), dim3(256), 0, stream,
+                     reinterpret_cast<const char*>(c.x), c.ldx * 2, x_rows, s.d_in, a.k_tiles * kW4K, c.ws + pl.xs,
+                     reinterpret_cast<float*>(c.ws + pl.up), g);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  a.tiles_o = (s.d_out + kCols - 1) / kCols;
+  a.tiles_t = (c.R + pl.bm - 1) / pl.bm;
+  if (c.ids != nullptr) {
     hipLaunchKernelGGL(w4_place_kernel, dim3((unsigned)g.chunks), dim3(kGroupThreads), 0, stream, g);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     a.perm = g.perm;

@@ -24,7 +24,6 @@ __global__ __launch_bounds__(256) void w4_sum_kernel(const W4SumArgs p) {
   const int t = (int)blockIdx.x;
   if (o >= p.d_out) return;
   f32x4_t s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
   for (int j = 0; j < p.k; ++j) {
     const int64_t r = (int64_t)t * p.k + j;
     if (p.ids != nullptr && (unsigned)p.ids[r] >= (unsigned)p.n) continue;
