@@ -2,8 +2,8 @@
 //
 //   y[r, o] = sum_g s[o, g] sum_{k in g} (q[o, k] - z[o, g]) x[r, k]
 //
-// bounded by the matrix cores.  A workgroup takes 16 NT rows x 256 outputs,
-// each of its four waves 64 outputs of all the rows, so that a code is
+// bounded by the matrix cores and the unpacking beside them.  A workgroup takes
+// 16 NT rows x 256 outputs, each of its waves 32 or 64 outputs of all the rows, so that a code is
 // unpacked once per 16 NT rows; the waves share the rows of x in LDS, staged
 // 128 inputs at a time by loads that write LDS directly, two buffers.
 //
@@ -201,8 +201,14 @@ struct W4GemmArgs {
   int per_split;  // tiles of inputs per split (blockIdx.y): float32 rows [splits][R]
 };
 
-constexpr int kWaves = 4, kRT = 4;  // waves; blocks of 16 outputs per wave
-constexpr int kCols = kWaves * kRT * 16;
+constexpr int kCols = 256;  // outputs of a workgroup
+// Its waves, each with kCols / waves of the outputs.  Eight waves of two
+// 16-output blocks fit four to a SIMD, four waves of four blocks two; with
+// more than one scale per tile and output eight no longer fit their
+// registers.  Measured (8, 4 waves): 8192 rows 4096 -> 14336 863, 899 us, with
+// groups of 64 and zero points 1093, 1028, of 32 1451, 1172; 32 experts of 512
+// rows 2048 -> 2816 244, 265.
+constexpr int gemm_waves(int sub) { return sub == 1 ? 8 : 4; }
 constexpr int kTileOrder = 4;  // row tiles walked together (w4_tile_of)
 
 // Block b -> tile, as for the bf16 base product: each XCD (b % 8) takes a run
@@ -225,6 +231,11 @@ __device__ __forceinline__ void dma16(rsrc_t r, char* dst, uint32_t voff, uint32
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, soff, 0, 0);
 }
 
+template <int NT, int kWaves>
+constexpr int x_loads() {  // of a wave and step
+  static_assert(4 * NT % kWaves == 0, "every wave loads the same number of rows");
+  return 4 * NT / kWaves;
+}
 template <int NT>
 constexpr int stage_bytes() {
   return 16 * NT * kW4K * 2;
@@ -234,15 +245,15 @@ constexpr int stage_bytes() {
 // registers.  `rd` and `wr` (where the next rows are being written) are
 // different buffers, which restrict tells the compiler, so that no read waits
 // for the loads in flight.
-template <int KIND, int SUB, int NT>
+template <int SUB, int NT, int kWaves, int kRT>
 __device__ __forceinline__ void gemm_step(const char* __restrict__ rd, char* __restrict__ wr, bool more,
-                                          rsrc_t xr, const uint32_t (&src)[NT], uint32_t soff, const uint4 (&b)[kRT][4],
+                                          rsrc_t xr, const uint32_t (&src)[x_loads<NT, kWaves>()], uint32_t soff, const uint4 (&b)[kRT][4],
                                           const float (&sc)[kRT][SUB], uint32_t lane_row, int h, int row16,
                                           f32x4_t (&acc)[NT][kRT]) {
   constexpr int kSteps = 4 / SUB;
   if (more)
 #pragma unroll
-    for (int q = 0; q < NT; ++q) dma16(xr, wr + q * 1024 * kWaves, src[q], soff);
+    for (int q = 0; q < x_loads<NT, kWaves>(); ++q) dma16(xr, wr + q * 1024 * kWaves, src[q], soff);
   __builtin_amdgcn_s_setprio(1);  // a wave with products ahead goes before one that unpacks
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -267,8 +278,10 @@ __device__ __forceinline__ void gemm_step(const char* __restrict__ rd, char* __r
 }
 
 template <int KIND, int SUB, int NT, bool F32OUT>
-__global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ __launch_bounds__(64 * gemm_waves(SUB))
+__attribute__((amdgpu_waves_per_eu(gemm_waves(SUB) / 2, gemm_waves(SUB) / 2)))
 void w4_gemm_kernel(const W4GemmArgs p) {
+  constexpr int kWaves = gemm_waves(SUB), kRT = kCols / 16 / kWaves;  // blocks of 16 outputs per wave
   constexpr int kRows = 16 * NT;
   __shared__ __align__(16) char lds[2 * stage_bytes<NT>()];
   const int tid = (int)threadIdx.x, lane = tid & 63;
@@ -300,15 +313,15 @@ void w4_gemm_kernel(const W4GemmArgs p) {
   // matrix-core read lie on all banks.  Rows past m repeat the last.
   const uint32_t x_bytes = p.k_tiles * kW4K * 2;
   const rsrc_t xr = make_rsrc(p.xs, (uint32_t)(p.R / p.x_div) * x_bytes);  // below 2^32 (w4_plan_call)
-  uint32_t src[NT];
+  uint32_t src[x_loads<NT, kWaves>()];
 #pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    const int row = 16 * q + 4 * w + (lane >> 4);
+  for (int q = 0; q < x_loads<NT, kWaves>(); ++q) {
+    const int row = 4 * (kWaves * q + w) + (lane >> 4);
     const int pos = pos0 + min(row, m - 1);
     const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos] : (uint32_t)pos;
     src[q] = (r / (uint32_t)p.x_div) * x_bytes + (((lane & 15) ^ (row & 15)) << 4);
   }
-  char* fill = lds + 1024 * w;  // + q * 4096: rows 16 q + 4 w ..
+  char* fill = lds + 1024 * w;  // + q * 1024 kWaves: rows 4 (kWaves q + w) ..
   const uint32_t lane_row = col * kW4K * 2;
 
   // ---- codes: one tile of each of the wave's four output blocks, loaded a
@@ -341,7 +354,7 @@ void w4_gemm_kernel(const W4GemmArgs p) {
 
   const int k0 = (int)blockIdx.y * p.per_split, k1 = min(p.k_tiles, k0 + p.per_split);
 #pragma unroll
-  for (int q = 0; q < NT; ++q) dma16(xr, fill + q * 1024 * kWaves, src[q], (uint32_t)k0 * kW4K * 2);
+  for (int q = 0; q < x_loads<NT, kWaves>(); ++q) dma16(xr, fill + q * 1024 * kWaves, src[q], (uint32_t)k0 * kW4K * 2);
   fetch(k0);
   for (int kt = k0; kt < k1; ++kt) {
     const bool more = kt + 1 < k1;
@@ -374,7 +387,7 @@ void w4_gemm_kernel(const W4GemmArgs p) {
     // go straight into the registers that have just been read.
     fetch(more ? kt + 1 : kt);
     const int cur = (kt - k0) & 1;
-    gemm_step<KIND, SUB, NT>(lds + cur * stage_bytes<NT>(), fill + (cur ^ 1) * stage_bytes<NT>(), more, xr, src,
+    gemm_step<SUB, NT, kWaves, kRT>(lds + cur * stage_bytes<NT>(), fill + (cur ^ 1) * stage_bytes<NT>(), more, xr, src,
                              (uint32_t)(kt + 1) * kW4K * 2, b, sc, lane_row, h, col, acc);
   }
 
@@ -397,7 +410,8 @@ void w4_gemm_kernel(const W4GemmArgs p) {
         }
       }
   } else {
-    constexpr int kLd = 64 * 2 + 16;  // bytes per row of the wave's block
+    constexpr int kPieces = 2 * kRT, kRowsAt = 64 / kPieces;  // 16-byte pieces per row of the wave's block
+    constexpr int kLd = 16 * kPieces + 16;                     // its bytes per row in LDS
     static_assert(kWaves * 16 * kLd <= 2 * stage_bytes<NT>(), "the output block fits the stage buffers");
     __syncthreads();  // x has been read
     char* mine = lds + w * 16 * kLd;
@@ -415,12 +429,12 @@ void w4_gemm_kernel(const W4GemmArgs p) {
       }
       asm volatile("" ::: "memory");  // a wave's LDS operations are in order
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int row = 8 * i + (lane >> 3), o = o0 + 64 * w + 8 * (lane & 7);
+      for (int i = 0; i < 16 / kRowsAt; ++i) {
+        const int row = kRowsAt * i + lane / kPieces, piece = lane % kPieces, o = o0 + 16 * kRT * w + 8 * piece;
         if (16 * t + row < m && o < p.d_out) {
           const int pos = pos0 + 16 * t + row;
           const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos] : (uint32_t)pos;
-          st16(p.y + (int64_t)r * p.ldy_bytes + 2 * (int64_t)o, ld16(mine + row * kLd + 16 * (lane & 7)));
+          st16(p.y + (int64_t)r * p.ldy_bytes + 2 * (int64_t)o, ld16(mine + row * kLd + 16 * piece));
         }
       }
       asm volatile("" ::: "memory");
@@ -433,8 +447,8 @@ hipError_t launch_nt(const W4GemmArgs& a, bool f32_out, hipStream_t stream) {
   const int64_t grid = (int64_t)a.tiles_o * a.tiles_t;
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   const unsigned splits = (unsigned)((a.k_tiles + a.per_split - 1) / a.per_split);
-  if (f32_out) hipLaunchKernelGGL((w4_gemm_kernel<KIND, SUB, NT, true>), dim3((unsigned)grid, splits), dim3(64 * kWaves), 0, stream, a);
-  else hipLaunchKernelGGL((w4_gemm_kernel<KIND, SUB, NT, false>), dim3((unsigned)grid, splits), dim3(64 * kWaves), 0, stream, a);
+  if (f32_out) hipLaunchKernelGGL((w4_gemm_kernel<KIND, SUB, NT, true>), dim3((unsigned)grid, splits), dim3(64 * gemm_waves(SUB)), 0, stream, a);
+  else hipLaunchKernelGGL((w4_gemm_kernel<KIND, SUB, NT, false>), dim3((unsigned)grid, splits), dim3(64 * gemm_waves(SUB)), 0, stream, a);
   return hipGetLastError();
 }
 template <int KIND, int SUB>
