@@ -277,7 +277,7 @@ void w4_rows_kernel(const W4RowsArgs p) {
       }
 #pragma unroll
       for (int a = 0; a < RT; ++a) {
-        code[u][a] = ld16_stream(code0[a] + (mat * p.code_stride + (int64_t)kt * kW4TileBytes) + lane16);
+        code[u][a] = ld16(code0[a] + (mat * p.code_stride + (int64_t)kt * kW4TileBytes) + lane16);
         par[u][a].load(par0[a] + (mat * p.param_stride + (int64_t)kt * (kW4Rows * W4Params<KIND, SUB>::kBytes)) + lane_par);
       }
     };
@@ -464,7 +464,7 @@ hipError_t launch_mode(const W4RowsArgs& a, const W4Plan& pl, unsigned gy, hipSt
     if (pl.chunked) return launch_one<E, KIND, SUB, 4, 1, 1, 4, MODE, true>(a, gy, stream);
     switch (pl.rt) {
       case 0: return launch_one<E, KIND, SUB, 1, 1, 2, 8, MODE, false>(a, gy, stream);
-      case 1: return launch_one<E, KIND, SUB, 1, 1, 4, 4, MODE, false>(a, gy, stream);
+      case 1: return launch_one<E, KIND, SUB, 1, 1, 4, 8, MODE, false>(a, gy, stream);
       case 2: return launch_one<E, KIND, SUB, 2, 1, 2, 4, MODE, false>(a, gy, stream);
       default: return launch_one<E, KIND, SUB, 4, 1, 1, 4, MODE, false>(a, gy, stream);
     }

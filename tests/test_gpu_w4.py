@@ -82,6 +82,15 @@ DENSE = [
     (513, 776, 328, 64, True, "bf16", "bf16"),
     (1030, 512, 776, 32, True, "f32", "bf16"),
     (2049, 264, 1096, 128, False, "bf16", "bf16"),
+    (16, 2056, 136, 64, True, "bf16", "bf16"),
+    (13, 4104, 72, 32, True, "bf16", "bf16"),
+    (16, 4096, 40, 128, False, "f32", "bf16"),
+    (30, 4104, 136, 64, True, "bf16", "bf16"),
+    (64, 3000, 72, 128, False, "bf16", "bf16"),
+    (800, 1032, 64, 32, True, "bf16", "bf16"),
+    (5, 2056, 40, 64, True, "f32", "f32"),
+    (9, 2056, 136, 128, False, "bf16", "f32"),
+    (40, 1032, 24, 32, True, "f32", "f32"),
     (1, 8, 8, 32, True, "f32", "f32"),
     (1, 1040, 136, 128, False, "f32", "f32"),
     (5, 520, 72, 32, True, "bf16", "f32"),
@@ -191,6 +200,11 @@ EXPERTS = [
     (700, 2, 5, 384, 328, 128, False, "bf16", "bf16", False, False),
     (1500, 3, 17, 136, 72, 32, True, "f32", "bf16", True, False),
     (120, 4, 8, 264, 72, 64, True, "bf16", "f32", False, True),
+    (3, 8, 20, 4104, 40, 128, True, "bf16", "bf16", True, True),
+    (1, 9, 9, 1032, 24, 64, False, "f32", "f32", True, True),
+    (30, 1, 1, 1032, 64, 32, True, "bf16", "bf16", False, False),
+    (40, 2, 2, 776, 72, 64, False, "bf16", "bf16", True, True),
+    (3000, 2, 300, 136, 24, 64, True, "bf16", "bf16", False, False),
 ]
 
 
@@ -354,6 +368,71 @@ def test_routed_layer():
     # experts' ids also group rows for adapters of the experts
     seg = rs.lora_segment(ids.flatten(), E)
     assert int(seg.seg_off[E]) == T * k and int(seg.n_invalid[0]) == 0
+
+
+def test_rows_beyond_32_bits():
+    """y, then x, of more than 2^32 bytes: the last rows are those of a call
+    of their own, the rows before them are written."""
+    dev = device()
+    T = 1 << 20
+    packed, s, z = make(90, 1, 2304, 64, 32, True, "bf16")
+    st = pack(packed, s, z, 32, "bf16", dev)
+    x = torch.randn(T, 64, device=dev).bfloat16()
+    note("w4 y of 4.8 GB")
+    y = rs.lora_w4_apply(st, x)
+    for at in (0, 777777, T - 4):
+        xs = x[at: at + 4].float().cpu().numpy()
+        a = (packed[0], s[0], z[0], 32, xs)
+        assert_close(y[at: at + 4], w4_apply_ref(*a), w4_magnitude_ref(*a), 64, 32, "bf16")
+    del x, y
+    packed, s, z = make(91, 1, 16, 2304, 64, True, "bf16")
+    st = pack(packed, s, z, 64, "bf16", dev)
+    note("w4 x of 4.8 GB")
+    x = torch.randn(T, 2304, device=dev, dtype=torch.bfloat16)
+    y = rs.lora_w4_apply(st, x)
+    for at in (0, 931234, T - 4):
+        xs = x[at: at + 4].float().cpu().numpy()
+        a = (packed[0], s[0], z[0], 64, xs)
+        assert_close(y[at: at + 4], w4_apply_ref(*a), w4_magnitude_ref(*a), 2304, 64, "bf16")
+    del x, y
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T", [2, 40, 300])
+def test_scales_and_zeros_that_are_special(T):
+    """Scales of zero, negative and very small; codes equal to their zero
+    point in whole groups; a group's last inputs missing."""
+    dev = device()
+    d_in, d_out, group = 200, 40, 64
+    packed, s, z = make(92, 1, d_out, d_in, group, True, "f32")
+    s[0, 0] = 0.0
+    s[0, 1] *= -1
+    s[0, 2] = 1e-30
+    s[0, 3, 1] = 0.0
+    packed[0, 4], z[0, 4] = 0xBB, 11
+    packed[0, 5], z[0, 5] = 0x00, 15
+    st = pack(packed, s, z, group, "f32", dev)
+    x = acts(93, T, d_in, "bf16")
+    y = rs.lora_w4_apply(st, torch.from_numpy(x).to(dev).bfloat16())
+    a = (packed[0], s[0], z[0], group, x)
+    assert_close(y, w4_apply_ref(*a), w4_magnitude_ref(*a), d_in, group, "bf16")
+    assert bool((y[:, 0] == 0).all())
+
+
+def test_weights_that_are_special():
+    """A weight of zero drops a finite row; negative weights; every weight zero."""
+    dev = device()
+    for T in (2, 60, 200):
+        case = (T, 3, 4, 136, 40, 32, True, "bf16", "bf16", False, True)
+        packed, s, z, x, ids, w = experts_case(case, 94, dev, hole=False)
+        w[0], w[1, 0] = 0.0, -2.5
+        st = pack(packed, s, z, 32, "bf16", dev)
+        y = rs.lora_w4_apply_experts(st, torch.from_numpy(x).to(dev).bfloat16(), torch.from_numpy(ids).to(dev),
+                                     torch.from_numpy(w).to(dev))
+        ref = experts_ref(packed, s, z, 32, x, ids, w)
+        mag = experts_ref(packed, s, z, 32, x, ids, np.abs(w), product=w4_magnitude_ref)
+        assert_close(y, ref, mag, 136, 32, "bf16", k=3)
+        assert bool((y[0] == 0).all())
 
 
 def test_refused_on_the_gpu():
