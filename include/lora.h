@@ -602,15 +602,17 @@ typedef struct lora_w4_store {
   const void* params;
 } lora_w4_store;
 
-/* Most matrices of a store, and most rows (T, or T * k) of a call. */
+/* Most matrices of a store, largest d_in and d_out, and most rows (T, or
+ * T * k) of a call. */
 #define LORA_W4_MAX_N 1024
+#define LORA_W4_MAX_DIM (1 << 20)
 #define LORA_W4_MAX_ROWS (1 << 20)
 
 /*
  * Size query (host only): bytes of a w4 store's two buffers.  Errors:
  * INVALID_ARG (null outputs, n < 1, d < 1, group < 1, has_zeros not 0 or 1);
- * UNSUPPORTED (n above LORA_W4_MAX_N, d_in or d_out not a multiple of 8,
- * group not a multiple of 32, unknown scale dtype).
+ * UNSUPPORTED (n above LORA_W4_MAX_N, d_in or d_out not a multiple of 8 or
+ * above LORA_W4_MAX_DIM, group not a multiple of 32, unknown scale dtype).
  */
 int lora_w4_bytes(int n, int d_in, int d_out, int group, int scale_dtype, int has_zeros, size_t* code_bytes_host,
                   size_t* param_bytes_host);
@@ -650,7 +652,9 @@ size_t lora_w4_workspace_bytes(const lora_w4_store* store_host, int dtype, int T
  * scales in float32, and y rounds once.  Float32 x is taken in whole (as
  * three bf16 parts).  Results do not change from call to call.  A row of x
  * with an infinity or a NaN gives a row of y without finite values; other
- * rows are not touched by it.  Enqueues one to three kernels.
+ * rows are not touched by it.  (bf16 rows of few are multiplied with 32 + q
+ * and the excess taken off: a group whose |x| sum to more than 2^122 may
+ * overflow where the formula does not.)  Enqueues one to three kernels.
  * Errors: INVALID_ARG (null pointers, T < 0, ldx < d_in, ldy < d_out, a store
  * of several matrices, ws too small); UNSUPPORTED (sizes as lora_w4_bytes,
  * alignment, T above LORA_W4_MAX_ROWS).
@@ -669,10 +673,10 @@ int lora_w4_apply(const lora_w4_store* store_host, int dtype, const void* x, int
  *                  float32 in a fixed order and rounded once.
  * An id outside [0, n) names no matrix: its row of y is zero, and it adds
  * nothing to a sum whatever its weight (a token without any gets a row of
- * zeros); its x row is not read.  The same id may appear twice in a token.
+ * zeros), whatever its x row holds.  The same id may appear twice in a token.
  * Errors: as lora_w4_apply (a store of several matrices is what it is for);
  * INVALID_ARG for k < 1 or x_per_choice not 0 or 1; UNSUPPORTED for T k above
- * LORA_W4_MAX_ROWS.
+ * LORA_W4_MAX_ROWS.  Enqueues one to four kernels.
  */
 int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void* x, int64_t ldx, int x_per_choice,
                           void* y, int64_t ldy, int T, int k, const int32_t* ids, const float* weights, void* ws,
@@ -706,12 +710,14 @@ int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void
  * not a divisor of E, top_groups outside 1..groups, k above the experts of
  * top_groups groups, an unknown score); UNSUPPORTED (E above
  * LORA_ROUTE_MAX_EXPERTS, k above LORA_ROUTE_MAX_K, groups above
- * LORA_ROUTE_MAX_GROUPS, unknown dtype, misaligned pointers).
+ * LORA_ROUTE_MAX_GROUPS, T above LORA_ROUTE_MAX_TOKENS, unknown dtype,
+ * misaligned pointers).  Enqueues one kernel.
  */
 enum lora_route_score { LORA_ROUTE_SOFTMAX = 0, LORA_ROUTE_SIGMOID = 1 };
 #define LORA_ROUTE_MAX_EXPERTS 1024
 #define LORA_ROUTE_MAX_K 32
 #define LORA_ROUTE_MAX_GROUPS 64
+#define LORA_ROUTE_MAX_TOKENS (1 << 25)
 int lora_route(const void* logits, int64_t ldl, int dtype, int T, int E, int k, int score, const float* bias,
                int groups, int top_groups, int renormalize, float scale, int32_t* ids, float* weights, void* stream);
 

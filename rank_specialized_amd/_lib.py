@@ -57,12 +57,14 @@ class lora_w4_store(C.Structure):
 
 
 LORA_W4_MAX_N = 1024
+LORA_W4_MAX_DIM = 1 << 20
 LORA_W4_MAX_ROWS = 1 << 20
 LORA_ROUTE_SOFTMAX = 0
 LORA_ROUTE_SIGMOID = 1
 LORA_ROUTE_MAX_EXPERTS = 1024
 LORA_ROUTE_MAX_K = 32
 LORA_ROUTE_MAX_GROUPS = 64
+LORA_ROUTE_MAX_TOKENS = 1 << 25
 
 # name -> (restype, argtypes); mirrors include/lora.h
 P = C.c_void_p

@@ -17,7 +17,8 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 int check_w4_shape(int n, int d_in, int d_out, int group, int scale_dtype, int has_zeros) {
   if (n < 1 || d_in < 1 || d_out < 1 || group < 1 || (has_zeros != 0 && has_zeros != 1)) return LORA_ERR_INVALID_ARG;
   if (scale_dtype != LORA_DTYPE_BF16 && scale_dtype != LORA_DTYPE_F32) return LORA_ERR_UNSUPPORTED;
-  if (n > LORA_W4_MAX_N || d_in % 8 != 0 || d_out % 8 != 0 || group % 32 != 0) return LORA_ERR_UNSUPPORTED;
+  if (n > LORA_W4_MAX_N || d_in > LORA_W4_MAX_DIM || d_out > LORA_W4_MAX_DIM) return LORA_ERR_UNSUPPORTED;
+  if (d_in % 8 != 0 || d_out % 8 != 0 || group % 32 != 0) return LORA_ERR_UNSUPPORTED;
   return LORA_OK;
 }
 
@@ -151,7 +152,9 @@ int lora_route(const void* logits, int64_t ldl, int dtype, int T, int E, int k, 
     return LORA_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !ids || !weights)) return LORA_ERR_INVALID_ARG;
   if (dtype != LORA_DTYPE_BF16 && dtype != LORA_DTYPE_F32) return LORA_ERR_UNSUPPORTED;
-  if (E > LORA_ROUTE_MAX_EXPERTS || k > LORA_ROUTE_MAX_K || groups > LORA_ROUTE_MAX_GROUPS) return LORA_ERR_UNSUPPORTED;
+  if (E > LORA_ROUTE_MAX_EXPERTS || k > LORA_ROUTE_MAX_K || groups > LORA_ROUTE_MAX_GROUPS ||
+      T > LORA_ROUTE_MAX_TOKENS)
+    return LORA_ERR_UNSUPPORTED;
   if (!aligned(logits, (size_t)elem_bytes(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
     return LORA_ERR_UNSUPPORTED;
   if (T == 0) return LORA_OK;

@@ -23,7 +23,7 @@ struct W4PackArgs {
 // code of their zero point (a product of exactly zero with any finite x),
 // outputs past d_out code 0 with scale 0.
 __global__ __launch_bounds__(256) void w4_pack_kernel(const W4PackArgs p) {
-  const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t tile = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (tile >= p.tiles) return;
   const int lane = threadIdx.x & 63, row = lane & 15, h = lane >> 4;
   const int kt = (int)(tile % p.k_tiles);
@@ -91,7 +91,7 @@ hipError_t launch_w4_pack(const lora_w4_store& s, const uint8_t* q, const void* 
   a.d_in = s.d_in;
   a.d_out = s.d_out;
   a.group = s.group;
-  a.groups = (s.d_in + s.group - 1) / s.group;
+  a.groups = (s.d_in - 1) / s.group + 1;
   a.sub = w4_sub(s.group);
   a.kind = w4_param_kind(s.scale_dtype, s.has_zeros);
   a.k_tiles = w4_k_tiles(s.d_in);
@@ -99,9 +99,11 @@ hipError_t launch_w4_pack(const lora_w4_store& s, const uint8_t* q, const void* 
   a.tiles = (int64_t)s.n * w4_tiles(s.d_in, s.d_out);
   a.codes = reinterpret_cast<char*>(codes);
   a.params = reinterpret_cast<char*>(params);
-  const int64_t grid = (a.tiles + 3) / 4;
-  if (grid > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)grid), dim3(256), 0, stream, a);
+  // A grid holds less than 2^32 threads on an axis (64 GB of codes).
+  const int64_t blocks = (a.tiles + 3) / 4, gx = blocks < (1 << 20) ? blocks : 1 << 20;
+  const int64_t gy = (blocks + gx - 1) / gx;
+  if (gy > 65535) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(w4_pack_kernel, dim3((unsigned)gx, (unsigned)gy), dim3(256), 0, stream, a);
   return hipGetLastError();
 }
 

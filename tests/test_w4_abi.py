@@ -47,6 +47,34 @@ def test_bytes(lib):
     assert lib.lora_w4_bytes(1, 128, 16, 128, BF16, 0, None, None) == 1
 
 
+def test_sizes_at_their_limits(lib):
+    """The largest sizes that are taken give the bytes that they should; one
+    step more is refused, sizes near the largest int too."""
+    d, n, big = L.LORA_W4_MAX_DIM, L.LORA_W4_MAX_N, 2**31 - 8
+    c, p = C.c_size_t(), C.c_size_t()
+
+    def status(n, d_in, d_out, group=128, kind=(BF16, 0)):
+        return lib.lora_w4_bytes(n, d_in, d_out, group, *kind, C.byref(c), C.byref(p))
+
+    assert status(n, d, d, 32, (F32, 1)) == 0
+    assert (c.value, p.value) == (n * d * d // 2, n * d * (d // 32) * 8)
+    # 2^31 - 32 is 96 more than a multiple of 128: four scales per tile row (gcd 32) of 2 bytes
+    assert status(1, 64, 32, 2**31 - 32) == 0 and (c.value, p.value) == (2 * 1024, 2 * 16 * 4 * 2)
+    for bad in ((1, d + 8, 16), (1, 128, d + 8), (1, big, 16), (1, 128, big), (n + 1, 128, 16)):
+        assert status(*bad) == 2, bad
+        s = store(n=bad[0], d_in=bad[1], d_out=bad[2], group=128)
+        assert lib.lora_w4_workspace_bytes(C.byref(s), BF16, 4, 0, 0) == 0
+    for T in (1, 16, 128, 4096, L.LORA_W4_MAX_ROWS):
+        for k in (0, 1):
+            for dt in (BF16, F32):  # the plan of every call that is taken can be made
+                s = store(n=1 if k == 0 else n, d_in=d, d_out=d)
+                assert 0 <= lib.lora_w4_workspace_bytes(C.byref(s), dt, T, k, k) < 1 << 56
+    fake = 0x10000
+    for T, want in ((0, 0), (L.LORA_ROUTE_MAX_TOKENS + 1, 2), (2**31 - 1, 2)):
+        assert lib.lora_route(fake, 8, BF16, T, 8, 2, 0, None, 1, 1, 1, 1.0, fake, fake, None) == want
+    assert lib.lora_last_hip_error() == 0
+
+
 def test_pack_refusals(lib):
     out = L.lora_w4_store()
 
