@@ -115,12 +115,20 @@ inline W4Plan w4_plan_call(const lora_w4_store& s, int dtype, int T, int k, bool
       p.splits = (kt + p.per_split - 1) / p.per_split;
     }
   } else {
-    // A matrix's rows, with room for more than the average.
-    const int rows = k > 0 ? (by_row ? (R < 4 ? R : 4) : per + 3) : R;
+    // A matrix's rows, with room for more than the average: what does not fit
+    // takes the matrix's codes once more.  Uniform choices, and all rows of one
+    // matrix: 256 rows of 64 matrices 1408 -> 2048 25.6 and 128 us with 7 rows,
+    // 22.8 and 80 with 16 (256 rows 2048 -> 2816, in chunks with 16: 38 and 155,
+    // 39.6 and 79; float32 in chunks is slower, 128 rows 1408 -> 2048 35
+    // against 46); 64 rows of 64 2048 -> 2816 24.2 and 58 with 4, 24.2 and 36
+    // with 8, 29.7 and 21 with 16.
+    const int row_bytes = w4_lds_row_bytes(dtype, kt);
+    const int by_row_cap = 8 * (int64_t)row_bytes <= 64 * 1024 ? 8 : 4;
+    const int rows = k > 0 ? (by_row ? (R < by_row_cap ? R : by_row_cap) : (per < 13 && (bf16 || 16 * row_bytes <= 64 * 1024) ? 16 : per + 3)) : R;
     const int64_t blocks = (int64_t)row_tiles * (by_row ? R : (k > 0 ? (R < s.n ? R : s.n) : 1));
     p.nt = rows <= 16 ? 1 : (rows <= 32 || !bf16 ? 2 : 4);
     p.row_cap = rows < 16 * p.nt ? rows : 16 * p.nt;
-    const int64_t all = (int64_t)p.row_cap * w4_lds_row_bytes(dtype, kt);
+    const int64_t all = (int64_t)p.row_cap * row_bytes;
     // All inputs of the rows in LDS, where that leaves room for two
     // workgroups on a compute unit, or there is no more than one for it: 16
     // rows 3584 -> 3584 6.6 us so, 7.1 + 2.8 (and a sum) in chunks and
@@ -137,6 +145,7 @@ inline W4Plan w4_plan_call(const lora_w4_store& s, int dtype, int T, int k, bool
       // of at least eight tiles of inputs: 23 rows 18944 -> 3584 16.2 us with
       // 13 splits, 22 with 5.
       p.chunked = true;
+      p.row_cap = 16 * p.nt;
       p.rt = p.nt == 4 ? 2 : 4;
       const int64_t groups = (blocks + p.rt - 1) / p.rt * (k > 0 ? 1 : (R + p.row_cap - 1) / p.row_cap);
       int64_t want = (768 + groups - 1) / groups;
