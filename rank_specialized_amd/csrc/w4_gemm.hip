@@ -284,6 +284,8 @@ void w4_gemm_kernel(const W4GemmArgs p) {
   constexpr int kWaves = gemm_waves(SUB), kRT = kCols / 16 / kWaves;  // blocks of 16 outputs per wave
   constexpr int kRows = 16 * NT;
   __shared__ __align__(16) char lds[2 * stage_bytes<NT>()];
+  __shared__ uint32_t row_of[kRows];  // rows of y
+  __shared__ float row_up[kRows];     // and their powers of two
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, h = lane >> 4;
@@ -356,6 +358,12 @@ void w4_gemm_kernel(const W4GemmArgs p) {
 #pragma unroll
   for (int q = 0; q < x_loads<NT, kWaves>(); ++q) dma16(xr, fill + q * 1024 * kWaves, src[q], (uint32_t)k0 * kW4K * 2);
   fetch(k0);
+  for (int i = tid; i < kRows; i += 64 * kWaves) {  // published by a later barrier
+    const int pos = pos0 + min(i, m - 1);
+    const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos] : (uint32_t)pos;
+    row_of[i] = r;
+    row_up[i] = p.up[r / (uint32_t)p.x_div];
+  }
   for (int kt = k0; kt < k1; ++kt) {
     const bool more = kt + 1 < k1;
     // This step's x and codes were asked for a whole step ago; every wave has
@@ -391,54 +399,35 @@ void w4_gemm_kernel(const W4GemmArgs p) {
                              (uint32_t)(kt + 1) * kW4K * 2, b, sc, lane_row, h, col, acc);
   }
 
-  // ---- y: times the row's power of two.  bf16 goes through LDS, so that a
-  // row's 64 outputs of a wave leave as whole 128-byte lines.
-  if constexpr (F32OUT) {
+  // ---- y: times the row's power of two, through LDS, so that a row's outputs
+  // of a wave leave 16 bytes per lane, as whole lines.
+  constexpr int kEb = F32OUT ? 4 : 2, kPieces = kRT * kEb, kRowsAt = 64 / kPieces;  // 16-byte pieces per row
+  constexpr int kLd = 16 * kPieces + 16;                                           // its bytes per row in LDS
+  static_assert(kWaves * 16 * kLd <= 2 * stage_bytes<NT>(), "the output block fits the stage buffers");
+  __syncthreads();  // x has been read
+  char* mine = lds + w * 16 * kLd;
+  char* y = p.y + (F32OUT ? (int64_t)blockIdx.y * p.R * p.ldy_bytes : 0);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int row = 16 * t + 4 * h + v;
-        if (row >= m) continue;
-        const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos0 + row] : (uint32_t)(pos0 + row);
-        const float u = p.up[r / (uint32_t)p.x_div];
-        float* yrow = reinterpret_cast<float*>(p.y + ((int64_t)blockIdx.y * p.R + r) * p.ldy_bytes);
+    for (int v = 0; v < 4; ++v) {
+      const float u = row_up[16 * t + 4 * h + v];
 #pragma unroll
-        for (int a = 0; a < kRT; ++a) {
-          const int o = o0 + 16 * (kRT * w + a) + col;
-          if (o < p.d_out) yrow[o] = acc[t][a][v] * u;
-        }
+      for (int a = 0; a < kRT; ++a) {
+        char* at = mine + (4 * h + v) * kLd + kEb * (16 * a + col);
+        if constexpr (F32OUT) *reinterpret_cast<float*>(at) = acc[t][a][v] * u;
+        else *reinterpret_cast<uint16_t*>(at) = (uint16_t)f32_to_bf16(acc[t][a][v] * u);
       }
-  } else {
-    constexpr int kPieces = 2 * kRT, kRowsAt = 64 / kPieces;  // 16-byte pieces per row of the wave's block
-    constexpr int kLd = 16 * kPieces + 16;                     // its bytes per row in LDS
-    static_assert(kWaves * 16 * kLd <= 2 * stage_bytes<NT>(), "the output block fits the stage buffers");
-    __syncthreads();  // x has been read
-    char* mine = lds + w * 16 * kLd;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int row = 16 * t + 4 * h + v;
-        const int pos = pos0 + min(row, m - 1);
-        const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos] : (uint32_t)pos;
-        const float u = p.up[r / (uint32_t)p.x_div];
-#pragma unroll
-        for (int a = 0; a < kRT; ++a)
-          *reinterpret_cast<uint16_t*>(mine + (4 * h + v) * kLd + 2 * (16 * a + col)) = (uint16_t)f32_to_bf16(acc[t][a][v] * u);
-      }
-      asm volatile("" ::: "memory");  // a wave's LDS operations are in order
-#pragma unroll
-      for (int i = 0; i < 16 / kRowsAt; ++i) {
-        const int row = kRowsAt * i + lane / kPieces, piece = lane % kPieces, o = o0 + 16 * kRT * w + 8 * piece;
-        if (16 * t + row < m && o < p.d_out) {
-          const int pos = pos0 + 16 * t + row;
-          const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos] : (uint32_t)pos;
-          st16(p.y + (int64_t)r * p.ldy_bytes + 2 * (int64_t)o, ld16(mine + row * kLd + 16 * piece));
-        }
-      }
-      asm volatile("" ::: "memory");
     }
+    asm volatile("" ::: "memory");  // a wave's LDS operations are in order
+#pragma unroll
+    for (int i = 0; i < 16 / kRowsAt; ++i) {
+      const int row = kRowsAt * i + lane / kPieces, piece = lane % kPieces;
+      const int o = o0 + 16 * kRT * w + (16 / kEb) * piece;
+      if (16 * t + row < m && o < p.d_out)
+        st16(y + (int64_t)row_of[16 * t + row] * p.ldy_bytes + kEb * (int64_t)o, ld16(mine + row * kLd + 16 * piece));
+    }
+    asm volatile("" ::: "memory");
   }
 }
 
