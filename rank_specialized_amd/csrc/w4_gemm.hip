@@ -310,24 +310,10 @@ void w4_gemm_kernel(const W4GemmArgs p) {
     return;
   }
 
-  // ---- x: a wave-wide load fills 1 KiB, four rows of 256 bytes; slot i % 16
-  // of a row holds piece (i % 16) ^ (row % 16), so that the 16 rows of one
-  // matrix-core read lie on all banks.  Rows past m repeat the last.
-  const uint32_t x_bytes = p.k_tiles * kW4K * 2;
-  const rsrc_t xr = make_rsrc(p.xs, (uint32_t)(p.R / p.x_div) * x_bytes);  // below 2^32 (w4_plan_call)
-  uint32_t src[x_loads<NT, kWaves>()];
-#pragma unroll
-  for (int q = 0; q < x_loads<NT, kWaves>(); ++q) {
-    const int row = 4 * (kWaves * q + w) + (lane >> 4);
-    const int pos = pos0 + min(row, m - 1);
-    const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos] : (uint32_t)pos;
-    src[q] = (r / (uint32_t)p.x_div) * x_bytes + (((lane & 15) ^ (row & 15)) << 4);
-  }
-  char* fill = lds + 1024 * w;  // + q * 1024 kWaves: rows 4 (kWaves q + w) ..
-  const uint32_t lane_row = col * kW4K * 2;
-
-  // ---- codes: one tile of each of the wave's four output blocks, loaded a
-  // step ahead.  A matrix's codes are below 2^32 bytes (w4_plan_call).
+  // ---- codes: one tile of each of the wave's output blocks, loaded a step
+  // ahead; the first before the rows are looked up (64 experts of 256 rows
+  // 1408 -> 2048 139 us so, 146 after).  A matrix's codes are below 2^32 bytes
+  // (w4_plan_call).
   uint4 code[kRT];
   W4Params<KIND, SUB> par[kRT];
   constexpr int kParBytes = kW4Rows * W4Params<KIND, SUB>::kBytes;  // of a tile
@@ -345,6 +331,25 @@ void w4_gemm_kernel(const W4GemmArgs p) {
       par[a].load(pr, lane_par, (tile0[a] + kt) * kParBytes);
     }
   };
+  const int k0 = (int)blockIdx.y * p.per_split, k1 = min(p.k_tiles, k0 + p.per_split);
+  fetch(k0);
+
+  // ---- x: a wave-wide load fills 1 KiB, four rows of 256 bytes; slot i % 16
+  // of a row holds piece (i % 16) ^ (row % 16), so that the 16 rows of one
+  // matrix-core read lie on all banks.  Rows past m repeat the last.
+  const uint32_t x_bytes = p.k_tiles * kW4K * 2;
+  const rsrc_t xr = make_rsrc(p.xs, (uint32_t)(p.R / p.x_div) * x_bytes);  // below 2^32 (w4_plan_call)
+  uint32_t src[x_loads<NT, kWaves>()];
+#pragma unroll
+  for (int q = 0; q < x_loads<NT, kWaves>(); ++q) {
+    const int row = 4 * (kWaves * q + w) + (lane >> 4);
+    const int pos = pos0 + min(row, m - 1);
+    const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos] : (uint32_t)pos;
+    src[q] = (r / (uint32_t)p.x_div) * x_bytes + (((lane & 15) ^ (row & 15)) << 4);
+  }
+  char* fill = lds + 1024 * w;  // + q * 1024 kWaves: rows 4 (kWaves q + w) ..
+  const uint32_t lane_row = col * kW4K * 2;
+
   const uint32_t mask_a = w4_scalar(kCodeMask), mask_b = w4_scalar(kCodeMask << 4);
   const uint32_t magic_a = w4_vector(kMagicF16A), magic_b = w4_vector(kMagicF16B);
 
@@ -354,10 +359,8 @@ void w4_gemm_kernel(const W4GemmArgs p) {
 #pragma unroll
     for (int a = 0; a < kRT; ++a) acc[t][a] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const int k0 = (int)blockIdx.y * p.per_split, k1 = min(p.k_tiles, k0 + p.per_split);
 #pragma unroll
   for (int q = 0; q < x_loads<NT, kWaves>(); ++q) dma16(xr, fill + q * 1024 * kWaves, src[q], (uint32_t)k0 * kW4K * 2);
-  fetch(k0);
   for (int i = tid; i < kRows; i += 64 * kWaves) {  // published by a later barrier
     const int pos = pos0 + min(i, m - 1);
     const uint32_t r = p.perm != nullptr ? (uint32_t)p.perm[pos] : (uint32_t)pos;
