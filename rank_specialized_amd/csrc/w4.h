@@ -68,14 +68,15 @@ struct W4Plan {
 };
 // Rows of a weighted call up to which a token's k products are one
 // workgroup's sum (if its rows fit LDS).  8 experts of 1408 -> 2048 for one
-// token: 10.4 us in one kernel, 7.5 + 3.9 us as partial rows and their sum;
+// token: 9.4 us in one kernel, 7.5 + 3.9 us as partial rows and their sum;
 // the partial rows read a matrix once for all its tokens, though, so more
 // than a few tokens are better off with them.
 constexpr int kW4SumRows = 32;
 // Rows per tile of the many-rows kernel.  Larger tiles unpack a code for more
-// rows; 112 rows take every register there is.  Measured (64, 96, 112 rows):
-// 8192 rows, 4096 -> 14336: 1076, 905, 965 us; 32 experts of 512 rows, 2048 ->
-// 2816: 291, 272, 273 us; 64 experts of 256 rows, 1408 -> 2048: 202, 207, 221 us.
+// rows, smaller ones waste fewer rows of a matrix's last; 112 rows take every
+// register there is, and were slower than 96 in each of these.  Measured (64,
+// 96 rows): 8192 rows, 4096 -> 14336: 912, 871 us; 32 experts of 512 rows, 2048
+// -> 2816: 224, 222 us; 64 experts of 256 rows, 1408 -> 2048: 138, 143 us.
 constexpr int kW4BigTile = 96, kW4SmallTile = 64;
 constexpr int kW4BigRows = 384;  // rows per matrix from which the big tile is taken
 constexpr int kW4Chunk = 4096;  // rows sorted by one workgroup
@@ -93,9 +94,10 @@ inline W4Plan w4_plan_call(const lora_w4_store& s, int dtype, int T, int k, bool
   // The many-rows kernel: rows enough per matrix for its tiles, and tiles
   // enough for the GPU.  It has x rewritten first and, by matrix, the rows
   // sorted (5 to 20 us).  Few-rows against many-rows, all kernels: 32 experts
-  // of 12 rows 32 against 48 us, of 32 rows 116 against 88, of 64 rows 150
-  // against 95 (2048 -> 2816); 3584 -> 3584: 128 rows 21 against 34 us, 512
-  // rows 41 against 55; 256 rows of 3584 -> 18944 160 against 69.
+  // of 12 rows 30 against 45 us, of 24 rows 43 against 45, of 32 rows 90 against
+  // 64, of 64 rows 148 against 70 (2048 -> 2816); 3584 -> 3584: 128 rows 20
+  // against 27 us, 512 rows 36 against 37; 256 rows of 3584 -> 18944 93
+  // against 61.
   // Its offsets are 32-bit: the rewritten x and a matrix stay below 2^32 bytes.
   const int64_t xs_bytes = (int64_t)R * kt * kW4K * 2, matrix_bytes = w4_tiles(s.d_in, s.d_out) * kW4TileBytes;
   const int bm = per >= kW4BigRows ? kW4BigTile : kW4SmallTile;
@@ -131,19 +133,19 @@ inline W4Plan w4_plan_call(const lora_w4_store& s, int dtype, int T, int k, bool
     const int64_t all = (int64_t)p.row_cap * row_bytes;
     // All inputs of the rows in LDS, where that leaves room for two
     // workgroups on a compute unit, or there is no more than one for it: 16
-    // rows 3584 -> 3584 6.6 us so, 7.1 + 2.8 (and a sum) in chunks and
-    // splits; but 3584 -> 18944 31 against 13 + 3.9.
+    // rows 3584 -> 3584 5.8 us so, 7.1 + 2.8 (and a sum) in chunks and
+    // splits; but 3584 -> 18944 31 against 11.5 + 3.9.
     if (p.nt == 1 && (all <= 64 * 1024 || (blocks < 512 && all <= 128 * 1024))) {
       // 16-output blocks per workgroup: more share a row's LDS reads, fewer
       // give every compute unit work.  Waves and tiles in flight go with it
       // (launch_mode).  One token (blocks): 3584 -> 512 (32) 3.5, 5.4, 8.8 us
-      // with 1, 2, 4; 3584 -> 18944 (1184) 10.0, 11.1, 13.4; eight experts of
+      // with 1, 2, 4; 3584 -> 18944 (1184) 9.3, 11.1, 13.4; eight experts of
       // 2048 -> 2816 (1408) 10.6, 7.8, 10.2; 40 (7040) 43, 36, 27.
       p.rt = blocks < 512 ? 0 : (blocks < 1280 ? 1 : (blocks < 2816 ? 2 : 4));
     } else {
       // In chunks, and the inputs split until there are about 768 workgroups
-      // of at least eight tiles of inputs: 23 rows 18944 -> 3584 16.2 us with
-      // 13 splits, 22 with 5.
+      // of at least eight tiles of inputs: 23 rows 18944 -> 3584 14.0 us with
+      // 13 splits, 19.2 with 6.
       p.chunked = true;
       p.row_cap = 16 * p.nt;
       p.rt = p.nt == 4 ? 2 : 4;

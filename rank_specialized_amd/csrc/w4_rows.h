@@ -15,7 +15,14 @@
 // every call; splits leave float32 rows that a last kernel adds in order.
 // (With x loaded from memory beside the codes, a lane's four 16-byte pieces
 // of x per tile took four times the registers of the codes and as many passes
-// through the load path: 19.0 us for one token, 3584 -> 18944, against 10.0.)
+// through the load path: 19.0 us for one token, 3584 -> 18944, against 9.3.)
+//
+// Measured (kernel times, weights not in the caches): one token 3584 -> 18944
+// 9.3 us (35.6 MB, 3.8 TB/s), 23 rows 18944 -> 3584 14.0 and 4.0 for the splits'
+// sum, 33 rows of 32 experts 8.0 for one token's eight of 64 (2048 -> 2816, 23.8
+// MB, 3.0 TB/s).  The loads of the codes go through the caches: past them (as
+// data read once) one token took 10.4, 23 rows 16.2.  More waves per workgroup
+// rather than more tiles per wave in flight: 8 waves of four 9.3 us, 4 waves 10.4.
 //
 // Products run on the matrix cores with x on the row side and the codes on
 // the column side, 16 rows x 16 outputs.  A code enters as the bf16 number
@@ -94,7 +101,7 @@ __device__ __forceinline__ int rows_of(const W4RowsArgs& p, int e, bool none, in
     cnt = total;
     __syncthreads();
   }
-  return cnt;
+  return __builtin_amdgcn_readfirstlane(cnt);  // the same in every lane: the loops over rows stay scalar
 }
 
 // Empty sums: outputs [o0, o0 + width) of `cnt` listed rows.
@@ -154,9 +161,7 @@ void w4_rows_kernel(const W4RowsArgs p) {
   extern __shared__ __align__(16) char lds[];
   __shared__ uint16_t list[kList ? kListMax : 1];
   __shared__ int s_cnt[W];
-  const int tid = (int)threadIdx.x, lane = tid & 63;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: the codes' addresses stay scalar
-  const int col = lane & 15, h = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);  // uniform: the codes' addresses stay scalar
   const int rt0 = (int)blockIdx.x * RT;
   // kSum: every tile of the token's rows, one row after the other
   const int t_begin = kSumUp ? 0 : (int)blockIdx.z * p.per_split;
@@ -170,6 +175,7 @@ void w4_rows_kernel(const W4RowsArgs p) {
     if (p.by_row && p.R <= 64) {
       // One id per lane: each wave finds its matrix and the rows that have it
       // by itself (all waves write the same list).
+      const int lane = (int)threadIdx.x & 63;
       const int id = lane < p.R ? p.ids[lane] : 0;
       e = __builtin_amdgcn_readlane(id, blockIdx.y);
       none = (unsigned)e >= (unsigned)p.n;
@@ -185,7 +191,6 @@ void w4_rows_kernel(const W4RowsArgs p) {
   }
   const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
   const uint32_t mask = w4_scalar(kCodeMask), magic = w4_vector(kMagicBf16);
-  const uint32_t lane16 = 16 * lane, lane_par = col * W4Params<KIND, SUB>::kBytes;
   const char *code0[RT], *par0[RT];  // first tile of each output block
 #pragma unroll
   for (int a = 0; a < RT; ++a) {
@@ -196,6 +201,13 @@ void w4_rows_kernel(const W4RowsArgs p) {
 
   // m rows from base (or from list[m0]): x into LDS, the products, y.
   auto block = [&](int base, int m0, int m) {
+    // A value the compiler cannot take out of the loop over a matrix's rows:
+    // what depends on the lane is formed again for each block, and does not
+    // hold registers across it.
+    int tid = (int)threadIdx.x;
+    if constexpr (kList) asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, col = lane & 15, h = lane >> 4;
+    const uint32_t lane16 = 16 * lane, lane_par = col * W4Params<KIND, SUB>::kBytes;
     const int x_rows = kSumUp ? (p.x_div == 1 ? p.k : 1) : m;
     auto x_row = [&](int i) {  // uniform
       uint32_t r = base + i;
