@@ -14,8 +14,8 @@
 // computed at the end, by the k lanes that hold the chosen logits.
 //
 // What bounds it is the length of a wave's chain, not the bytes: one token of
-// 64 experts 2.7 us (the shortest fill kernel: 1.3), 8192 tokens of 64 (4.7 MB)
-// 8.9, 252 tokens of 256 experts in groups with a bias 9.7, of which the
+// 64 experts 2.7 us (the shortest fill kernel: 1.3), 8192 tokens of 128 (4.7
+// MB) 8.9, 250 tokens of 256 experts in groups with a bias 9.7, of which the
 // float64 scores and eight choices of 64-bit keys are most.  So whatever is
 // independent is asked for, exchanged and computed side by side: 10.9 us with
 // the group scores one value after the other, 10.4 with a branch around each

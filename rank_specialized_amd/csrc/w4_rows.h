@@ -17,12 +17,16 @@
 // of x per tile took four times the registers of the codes and as many passes
 // through the load path: 19.0 us for one token, 3584 -> 18944, against 9.3.)
 //
-// Measured (kernel times, weights not in the caches): one token 3584 -> 18944
-// 9.3 us (35.6 MB, 3.8 TB/s), 23 rows 18944 -> 3584 14.0 and 4.0 for the splits'
-// sum, 33 rows of 32 experts 8.0 for one token's eight of 64 (2048 -> 2816, 23.8
-// MB, 3.0 TB/s).  The loads of the codes go through the caches: past them (as
-// data read once) one token took 10.4, 23 rows 16.2.  More waves per workgroup
-// rather than more tiles per wave in flight: 8 waves of four 9.3 us, 4 waves 10.4.
+// Measured (kernel times, three sets of weights in turn): one token 3584 ->
+// 18944 9.3 us (35.6 MB, 3.8 TB/s); 23 rows 18944 -> 3584 in groups of 64 14.0
+// (2.7) and 4.0 for the splits' sum; one token's eight experts of 64, 2048 ->
+// 2816, 7.9 (23.8 MB, 3.0), eight tokens' 28.7 (about 120 MB, 4.2); 180 rows
+// of 32 experts 1408 -> 2048 in groups of 32 18.0 (2.9): with few bytes the
+// launch, the copy of x and the last sums show, with fine groups the
+// instructions per code.  The codes' loads go through the caches (past them,
+// as data read once, one token took 10.4, the 23 rows 16.2).  More waves in a
+// workgroup rather than more tiles in a wave's flight: one token 9.3 us with
+// 8 waves of four tiles, 10.4 with 4.
 //
 // Products run on the matrix cores with x on the row side and the codes on
 // the column side, 16 rows x 16 outputs.  A code enters as the bf16 number
