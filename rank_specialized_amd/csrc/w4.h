@@ -110,12 +110,17 @@ inline double w4_few_us(int R, int64_t tiles) { return 9. + 5.8e-4 * (double)til
 // The many-rows kernel's tiles and splits, if it is taken.  It has x rewritten
 // first and, by matrix, the rows sorted (5 to 20 us).  By matrix, few-rows
 // against many-rows, all kernels: 32 experts of 12 rows 30 against 45 us, of 24
-// rows 43 against 45, of 32 rows 90 against 64, of 64 rows 148 against 70 (2048
-// -> 2816).  Of one matrix, what the two are expected to take.  Offsets are
-// 32-bit: the rewritten x and a matrix stay below 2^32 bytes.
+// rows 38 against 45, of 32 rows 90 against 64, of 64 rows 148 against 70 (2048
+// -> 2816); of a few small matrices up to 48 rows each, 26 and 48 rows: 3 of 512
+// -> 264 7.2, 7.6 against 15.6, 15.3; 8 of 1024 -> 1024 8.6, 10.2 against 17.6,
+// 19.1; 4 of 2048 -> 2048 13.0, 16.2 against 19.8, 22.5 (with many matrices the
+// rows of one that most choose would take long: 32 of 1024 -> 512, all rows of
+// one, 133 against 21).  Of one matrix, what the two are expected to take.
+// Offsets are 32-bit: the rewritten x and a matrix stay below 2^32 bytes.
 inline void w4_plan_many(W4Plan& p, const lora_w4_store& s, int R, int per, bool by_matrix, int64_t xs_bytes) {
-  if ((by_matrix ? per <= 24 : R <= 64) || xs_bytes >= ((int64_t)1 << 32)) return;
   const int64_t codes = w4_tiles(s.d_in, s.d_out);
+  const int few = s.n <= 8 && s.n * codes <= 8192 ? 48 : 24;
+  if ((by_matrix ? per <= few : R <= 64) || xs_bytes >= ((int64_t)1 << 32)) return;
   if (codes * kW4TileBytes >= ((int64_t)1 << 31)) return;
   const int kt = w4_k_tiles(s.d_in);
   double best = 0.;

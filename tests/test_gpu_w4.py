@@ -205,6 +205,10 @@ EXPERTS = [
     (30, 1, 1, 1032, 64, 32, True, "bf16", "bf16", False, False),
     (40, 2, 2, 776, 72, 64, False, "bf16", "bf16", True, True),
     (3000, 2, 300, 136, 24, 64, True, "bf16", "bf16", False, False),
+    (60, 1, 1, 1032, 64, 32, True, "bf16", "bf16", False, False),
+    (110, 2, 4, 1544, 72, 64, False, "bf16", "bf16", True, True),
+    (90, 3, 2, 1032, 136, 128, False, "f32", "bf16", False, True),
+    (260, 3, 12, 520, 264, 128, True, "bf16", "bf16", False, False),
 ]
 
 
