@@ -656,12 +656,24 @@ def _same_device(index: int, **tensors) -> None:
             raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
 
 
+_INT_MAX = 2**31 - 1  # what the C interface's sizes hold; ctypes would cut more off silently
+
+
+def _int(v, name: str) -> int:
+    v = int(v)
+    if not -_INT_MAX <= v <= _INT_MAX:
+        raise ValueError(f"{name} is out of range")
+    return v
+
+
 def _ld(t: torch.Tensor, name: str) -> int:
     """Row stride of a 2-D tensor with unit column stride; of at most one row,
     its length (its stride is then any number)."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with unit column stride")
     rows, cols = t.shape
+    if rows > _INT_MAX or cols > _INT_MAX:
+        raise ValueError(f"{name} has more rows or columns than an int counts")
     ld, step = t.stride()
     if rows > 0 and cols > 1 and step != 1:
         raise ValueError(f"{name} must be 2-D with unit column stride")
@@ -678,6 +690,7 @@ def _dtype(t: torch.Tensor, name: str) -> int:
 def lora_w4_bytes(n: int, d_in: int, d_out: int, group: int, scale_dtype: torch.dtype, has_zeros: bool):
     """Bytes of a w4 store's codes and params buffers."""
     a, b = C.c_size_t(), C.c_size_t()
+    n, d_in, d_out, group = _int(n, "n"), _int(d_in, "d_in"), _int(d_out, "d_out"), _int(group, "group")
     L.check("lora_w4_bytes", L.lib().lora_w4_bytes(n, d_in, d_out, group, _DTYPES[scale_dtype], int(has_zeros),
                                                    C.byref(a), C.byref(b)))
     return a.value, b.value
@@ -697,7 +710,7 @@ def lora_w4_pack(q: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Te
         raise ValueError("q must be uint8 [n, d_out, d_in / 2]")
     n, d_out, half = q.shape
     d_in = 2 * half
-    group = int(group)
+    group = _int(group, "group")
     if group < 1:
         raise ValueError("group must be positive")
     shape = (n, d_out, -(-d_in // group))
@@ -721,7 +734,7 @@ def lora_w4_pack(q: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Te
 
 def lora_w4_workspace_bytes(store: W4Store, dtype: torch.dtype, T: int, k: int = 0, weighted: bool = False) -> int:
     """Workspace of lora_w4_apply (k = 0) or lora_w4_apply_experts for T tokens."""
-    return int(L.lib().lora_w4_workspace_bytes(store.ref(), _DTYPES[dtype], int(T), int(k), int(weighted)))
+    return int(L.lib().lora_w4_workspace_bytes(store.ref(), _DTYPES[dtype], _int(T, "T"), _int(k, "k"), int(weighted)))
 
 
 def _w4_run(name: str, store: W4Store, x: torch.Tensor, rows: int, y, T: int, k: int, ids, weights, ws, middle):
@@ -777,6 +790,8 @@ def lora_w4_apply_experts(store: W4Store, x: torch.Tensor, ids: torch.Tensor, we
     if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 [T, k]")
     T, k = ids.shape
+    if k > _INT_MAX:
+        raise ValueError("ids has more columns than an int counts")
     x_rows = x.shape[0]
     if x_rows != T and x_rows != T * k:
         raise ValueError("x must be [T, d_in] or [T k, d_in]")
@@ -805,7 +820,7 @@ def lora_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Op
     mode = _SCORES.get(score)
     if mode is None:
         raise ValueError("score must be 'softmax' or 'sigmoid'")
-    k, index = int(k), logits.get_device()
+    k, index = _int(k, "k"), logits.get_device()
     if k < 1:
         raise ValueError("k must be positive")
     if bias is not None:
@@ -827,5 +842,5 @@ def lora_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Op
     else:
         _same_device(index, weights=weights)
     _call("lora_route", index, _p(logits), ldl, dt, T, E, k, mode, bias.data_ptr() if bias is not None else None,
-          int(groups), int(top_groups), int(renormalize), float(scale), _p(ids), _p(weights))
+          _int(groups, "groups"), _int(top_groups, "top_groups"), int(renormalize), float(scale), _p(ids), _p(weights))
     return ids, weights

@@ -225,3 +225,28 @@ def test_oracle_route():
     assert ids.tolist() == [[0]] and math.isclose(w[0, 0], 1 / (1 + math.e))
     ids, w = route_ref(np.full((1, 3), -math.inf), 2)
     assert ids.tolist() == [[-1, -1]] and not w.any()
+
+
+def test_sizes_beyond_an_int():
+    """ctypes cuts an int to 32 bits: the binding refuses what it would cut
+    (a group of 2^32 + 32 would read scales that are not there)."""
+    wrap = 2**32
+    q, s = torch.zeros(16, 64, dtype=torch.uint8), torch.ones(16, 1)
+    for bad in (wrap + 32, wrap + 128, -wrap + 32):
+        with pytest.raises(ValueError, match="group"):
+            rs.lora_w4_pack(q, s, group=bad)
+    for bad in ((wrap + 1, 128, 16, 128), (1, wrap + 128, 16, 128), (1, 128, wrap + 16, 128), (1, 128, 16, wrap + 128)):
+        with pytest.raises(ValueError, match="out of range"):
+            rs.lora_w4_bytes(*bad, torch.bfloat16, False)
+    long = torch.empty(1, 1, dtype=torch.bfloat16, device="meta").expand(2**31, 8)
+    wide = torch.empty(1, 1, dtype=torch.bfloat16, device="meta").expand(1, 2**31)
+    with pytest.raises(ValueError, match="more rows"):
+        rs.lora_w4_apply(None, long)
+    for bad in (long, wide):
+        with pytest.raises(ValueError, match="more rows"):
+            rs.lora_route(bad, 2)
+    ids = torch.empty(1, 2**31, dtype=torch.int32, device="meta")
+    with pytest.raises(ValueError, match="ids"):
+        rs.lora_w4_apply_experts(None, wide, ids)
+    with pytest.raises(ValueError, match="k is"):
+        rs.lora_route(torch.zeros(1, 8), wrap + 2)
