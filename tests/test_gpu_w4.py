@@ -421,6 +421,41 @@ def test_many_rows_captured_and_on_two_streams(T, d_in, d_out):
         assert np.array_equal(hbits(out), hbits(want[i]))
 
 
+def test_calls_of_several_threads():
+    """Four host threads, a stream and a size each, at once: the results of
+    calls made alone."""
+    import threading
+
+    dev = device()
+    sizes = [(1, 3592, 136), (40, 3592, 136), (16, 3592, 136), (300, 4104, 4104)]
+    jobs = []
+    for i, (T, d_in, d_out) in enumerate(sizes):
+        packed, s, z = make(110 + i, 1, d_out, d_in, 64, True, "bf16")
+        st = pack(packed, s, z, 64, "bf16", dev)
+        x = torch.from_numpy(acts(120 + i, T, d_in, "bf16")).to(dev).bfloat16()
+        jobs.append((st, x, rs.lora_w4_apply(st, x), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got, failed = [[] for _ in jobs], []
+
+    def work(i):
+        try:
+            st, x, _, stream = jobs[i]
+            with torch.cuda.stream(stream):
+                got[i] = [rs.lora_w4_apply(st, x) for _ in range(20)]
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for (_, _, want, _), ys in zip(jobs, got):
+        assert len(ys) == 20 and all(np.array_equal(hbits(y), hbits(want)) for y in ys)
+
+
 def test_routed_layer():
     """A layer as it is served: the base projection with the adapters' branch
     on it, the router, the experts' up product, and their weighted down
