@@ -306,7 +306,9 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs p) {
   if (lane < p.k) {
     const int64_t at = (int64_t)t * p.k + lane;
     p.ids[at] = id;
-    p.weights[at] = (float)(w * (double)p.scale);
+    // Without an expert w may be 0 / 0 (a softmax over none), or meet an
+    // infinite scale: the weight is 0 whatever it is.
+    p.weights[at] = have ? (float)(w * (double)p.scale) : 0.f;
   }
 }
 

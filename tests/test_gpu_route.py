@@ -148,3 +148,31 @@ def test_captured():
         want = rs.lora_route(l, 8, **kw)
         torch.cuda.synchronize()
         assert torch.equal(ids, want[0]) and torch.equal(w, want[1])
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rows_without_an_expert(score, renormalize, dtype):
+    """Rows with fewer experts than k, none among them, in every form: id -1
+    and weight 0 where there is none, whatever the scale."""
+    rng = np.random.default_rng(3)
+    l = rng.normal(size=(8, 40)).astype(np.float32)
+    l[0] = -np.inf
+    l[1] = np.nan
+    l[2, ::2], l[2, 1::2] = np.nan, -np.inf
+    l[3, 2:] = -np.inf
+    l[4, :39] = np.nan
+    l[5, 4:] = -np.inf
+    none = np.full(40, -np.inf)
+    some = 0.1 * rng.normal(size=40)
+    some[1:] = np.where(rng.random(39) < 0.9, -np.inf, some[1:])
+    for bias in (None, np.zeros(40), some, none):
+        for kw in (dict(), dict(groups=4, top_groups=2), dict(scale=2.5), dict(scale=-3.0, groups=5, top_groups=1)):
+            ids, w = check(l, dtype, 6, bias, score=score, renormalize=renormalize, **kw)
+            assert (ids[:3] == -1).all() and (w[:3] == 0).all()
+            assert bias is not none or (ids == -1).all()
+    dev = device()
+    for scale in (float("inf"), float("nan")):
+        ids, w = rs.lora_route(torch.from_numpy(l).to(dev), 6, score=score, renormalize=renormalize, scale=scale)
+        assert bool((w[ids < 0] == 0).all()) and int((ids < 0).sum()) >= 18
