@@ -702,8 +702,11 @@ int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void
  * Where fewer than k experts can be chosen, the rest of the row is id -1 and
  * weight 0.  A group with fewer than two experts that can be chosen comes
  * after every other in the sigmoid form (if it has two or more).
- * Comparisons involving the bias or sums are made in float64, so that the
- * choice is that of the formula, not of a rounding.
+ * Without a bias the order of c is that of the logits, whatever a score
+ * rounds to; a group's sum of two is compared in float64 where it is at most
+ * one and by what it lacks of two above.  With a bias c is formed in float64,
+ * and what is equal there is a tie: sigmoid scores of logits above 36.7 that
+ * have one bias, scores below 2^-53 of theirs.
  *   logits [T, ldl] : dtype rows, ldl >= E, naturally aligned (no 16-byte
  *            rule).
  * Errors: INVALID_ARG (null pointers, T < 0, E < 1, k < 1, ldl < E, groups

@@ -67,6 +67,18 @@ def experts_ref(packed, scales, zeros, group: int, x, ids, weights=None, product
     return y
 
 
+def pair_order(a: float, b: float):
+    """A key that orders as sigmoid(a) + sigmoid(b) does; -inf stands for no
+    logit, and sums without two come first.  A sum above one is its distance
+    from two, which a float holds where 1 - 2^-60 is not one."""
+    def sig(v):
+        return math.exp(v) / (1 + math.exp(v)) if v < 0 else 1 / (1 + math.exp(-v))
+
+    if min(a, b) == -math.inf:
+        return (-1, 0.0)
+    return (1, -(sig(-a) + sig(-b))) if a + b > 0 else (0, sig(a) + sig(b))
+
+
 def route_ref(logits, k: int, *, score="softmax", bias=None, groups=1, top_groups=1, renormalize=True, scale=1.0):
     """(ids [T, k], weights [T, k] float64), one token at a time."""
     T, E = logits.shape
@@ -98,10 +110,8 @@ def route_ref(logits, k: int, *, score="softmax", bias=None, groups=1, top_group
                     of.append(max(c[e] for e in part))
                 else:
                     two = sorted((c[e] for e in part), reverse=True)[:2]
-                    if bias is None:
-                        two = sorted((s[e] if c[e] > -math.inf else -math.inf for e in part), reverse=True)[:2]
-                    of.append(two[0] + two[1])
-            keep = sorted(range(groups), key=lambda g: (-of[g], g))[:top_groups]
+                    of.append(two[0] + two[1] if bias is not None else pair_order(*two))
+            keep = sorted(range(groups), key=lambda g: of[g], reverse=True)[:top_groups]  # stable: ties to the lowest
             c = [c[e] if e // n in keep else -math.inf for e in range(E)]
         order = [e for e in sorted(range(E), key=lambda e: (-c[e], e)) if c[e] > -math.inf][:k]
         w = [s[e] for e in order]

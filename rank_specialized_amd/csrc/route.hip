@@ -6,9 +6,12 @@
 // choice runs on integer keys that order as the numbers do (0: cannot be
 // chosen): without a bias, c orders as the logits themselves do, in both
 // scores, so the keys are the float32 logits and no score is computed for the
-// choice; with a bias, or where two scores are added (the sigmoid form's
-// groups), c is formed in float64, whose rounding is far below the distance
-// of different scores, so that the choice is the formula's.  Each of the k
+// choice.  Where a group's score is the sum of two sigmoids, that sum is
+// formed in float64 from its two largest logits, and above one from what the
+// two lack of one: sigmoids of more than 36.7 are 1.0 in float64 already.
+// With a bias c itself is formed in float64, and scores that are equal there
+// are ties (sigmoids above 36.7 with one bias, scores below 2^-53 of a bias).
+// Each of the k
 // steps takes the wave's largest key (four lane exchanges and a scalar
 // maximum of the four rows) and its lowest index, and drops it; weights are
 // computed at the end, by the k lanes that hold the chosen logits.
@@ -56,6 +59,7 @@ struct Key32 {
   __device__ bool above(Key32 o) const { return v > o.v; }
   __device__ bool same(Key32 o) const { return v == o.v; }
   __device__ static Key32 wave_largest(Key32 k) { return {wave_max(k.v)}; }
+  __device__ float value() const { return __uint_as_float((v & 0x80000000u) ? v & 0x7fffffffu : ~v); }
 };
 struct Key64 {
   uint64_t v;
@@ -82,8 +86,7 @@ struct Key64 {
 };
 
 __device__ __forceinline__ float wave_max_f(float v) {  // of numbers and -inf
-  const uint32_t k = wave_max(Key32::of(v).v);
-  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+  return Key32::wave_largest(Key32::of(v)).value();
 }
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
@@ -106,19 +109,38 @@ __device__ __forceinline__ uint64_t from_lane(uint64_t v, int l) {
   return ((uint64_t)from_lane((uint32_t)(v >> 32), l) << 32) | from_lane((uint32_t)v, l);
 }
 
-// A group's score from its largest and second largest key.
-template <typename Key>
-__device__ __forceinline__ Key group_score(Key a, Key b, bool pair) {
-  if constexpr (sizeof(Key) == 8) {
-    if (pair) return a.any() && b.any() ? Key::of(a.value() + b.value()) : Key::none();
+// A group's score from its largest and second largest key, where it is the
+// sum of two c (none, if there are no two).
+__device__ __forceinline__ Key64 pair_score(Key64 a, Key64 b) {
+  return a.any() && b.any() ? Key64::of(a.value() + b.value()) : Key64::none();
+}
+// The same from two logits, c = sigmoid: s(a) + s(b), which exceeds one where
+// a + b > 0, and is then 2 - (s(-a) + s(-b)): the keys of what is missing, in
+// reverse, behind that of one.  (a >= b; exp of at most 0 but for one term.)
+__device__ __forceinline__ Key64 pair_score(Key32 a, Key32 b) {
+  if (!a.any() || !b.any()) return Key64::none();
+  double x = (double)a.value(), y = (double)b.value();
+  const bool over = x + y > 0.0;
+  if (over) {
+    x = -x;
+    y = -y;
   }
-  return a;
+  const auto sigmoid = [](double v) {
+    const double e = exp(-fabs(v));
+    return (v > 0.0 ? 1.0 : e) / (1.0 + e);
+  };
+  const uint64_t s = Key64::of(sigmoid(x) + sigmoid(y)).v, one = Key64::of(1.0).v;
+  return {over ? one + (one - s) : s};
 }
 
-// WIDE: keys are the float64 c; else the logits.
-template <typename E, int NV, bool WIDE>
+// What the keys are: the logits; the logits, with groups by the sum of two
+// scores; or the float64 c.
+enum Keys { kLogits, kLogitPairs, kScores };
+template <typename E, int NV, Keys KEYS>
 __global__ __launch_bounds__(256) void route_kernel(const RouteArgs p) {
+  constexpr bool WIDE = KEYS == kScores;
   typedef typename std::conditional<WIDE, Key64, Key32>::type Key;
+  typedef typename std::conditional<KEYS == kLogits, Key32, Key64>::type GroupKey;
   const int lane = (int)threadIdx.x & 63;
   const int t = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6);
   if (t >= p.T) return;
@@ -171,8 +193,8 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs p) {
     // Group g's score on lane g (groups <= 64): its largest key, or the sum
     // of its two largest c.
     const int n = p.E / p.groups;
-    const bool pair = WIDE && !softmax && n > 1;
-    Key mine = Key::none();
+    const bool pair = KEYS == kLogitPairs || (WIDE && !softmax && n > 1);
+    Key first = Key::none(), second = Key::none();  // of the lane's group
     if (n <= 64 && (n & (n - 1)) == 0) {
       // A group is n neighbouring lanes of one value, and 64 / n groups are
       // reduced at once: (largest, second) pairs exchanged across n lanes.
@@ -202,11 +224,15 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs p) {
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        Key s = group_score(a[i], b[i], pair);
-        s.v = from_lane(s.v, (lane % per) * n);
-        if (lane / per == i) mine = s;
+        Key fa, fb = Key::none();
+        fa.v = from_lane(a[i].v, (lane % per) * n);
+        if (pair) fb.v = from_lane(b[i].v, (lane % per) * n);
+        if (lane / per == i) {
+          first = fa;
+          second = fb;
+        }
       }
-      if (lane >= p.groups) mine = Key::none();
+      if (lane >= p.groups) first = Key::none();
     } else {
       for (int g = 0; g < p.groups; ++g) {
         Key a = Key::none(), b = Key::none();
@@ -228,15 +254,20 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs p) {
           const uint64_t at = __ballot(a.same(top));
           rest = Key::wave_largest(lane == __ffsll((unsigned long long)at) - 1 ? b : a);
         }
-        const Key s = group_score(top, rest, pair);
-        if (lane == g) mine = s;
+        if (lane == g) {
+          first = top;
+          second = rest;
+        }
       }
     }
+    GroupKey mine;
+    if constexpr (KEYS == kLogits) mine = first;
+    else mine = pair ? pair_score(first, second) : GroupKey{first.v};
     // A group's rank: those with a larger score, or the same and a lower index.
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
-      Key o;
-      if constexpr (WIDE) {
+      GroupKey o;
+      if constexpr (sizeof(GroupKey) == 8) {
         o.v = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine.v >> 32), g) << 32) |
               (uint32_t)__builtin_amdgcn_readlane((int)mine.v, g);
       } else {
@@ -312,23 +343,28 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteArgs p) {
   }
 }
 
-template <typename E, bool WIDE>
+template <typename E, Keys KEYS>
 hipError_t launch_sized(const RouteArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)((a.T + 3) / 4)), block(256);
-  if (a.E <= 64) hipLaunchKernelGGL((route_kernel<E, 1, WIDE>), grid, block, 0, stream, a);
-  else if (a.E <= 128) hipLaunchKernelGGL((route_kernel<E, 2, WIDE>), grid, block, 0, stream, a);
-  else if (a.E <= 256) hipLaunchKernelGGL((route_kernel<E, 4, WIDE>), grid, block, 0, stream, a);
-  else if (a.E <= 512) hipLaunchKernelGGL((route_kernel<E, 8, WIDE>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((route_kernel<E, 16, WIDE>), grid, block, 0, stream, a);
+  if (a.E <= 64) hipLaunchKernelGGL((route_kernel<E, 1, KEYS>), grid, block, 0, stream, a);
+  else if (a.E <= 128) hipLaunchKernelGGL((route_kernel<E, 2, KEYS>), grid, block, 0, stream, a);
+  else if (a.E <= 256) hipLaunchKernelGGL((route_kernel<E, 4, KEYS>), grid, block, 0, stream, a);
+  else if (a.E <= 512) hipLaunchKernelGGL((route_kernel<E, 8, KEYS>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((route_kernel<E, 16, KEYS>), grid, block, 0, stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
+template <typename E>
+static hipError_t launch_type(const RouteArgs& a, hipStream_t stream) {
+  if (a.bias != nullptr) return launch_sized<E, kScores>(a, stream);
+  if (a.groups > 1 && a.groups < a.E && a.score == LORA_ROUTE_SIGMOID) return launch_sized<E, kLogitPairs>(a, stream);
+  return launch_sized<E, kLogits>(a, stream);
+}
+
 hipError_t launch_route(const RouteArgs& a, int dtype, hipStream_t stream) {
-  const bool wide = a.bias != nullptr || (a.groups > 1 && a.score == LORA_ROUTE_SIGMOID);
-  if (dtype == LORA_DTYPE_BF16) return wide ? launch_sized<BF16, true>(a, stream) : launch_sized<BF16, false>(a, stream);
-  return wide ? launch_sized<F32, true>(a, stream) : launch_sized<F32, false>(a, stream);
+  return dtype == LORA_DTYPE_BF16 ? launch_type<BF16>(a, stream) : launch_type<F32>(a, stream);
 }
 
 }  // namespace lora

@@ -176,3 +176,23 @@ def test_rows_without_an_expert(score, renormalize, dtype):
     for scale in (float("inf"), float("nan")):
         ids, w = rs.lora_route(torch.from_numpy(l).to(dev), 6, score=score, renormalize=renormalize, scale=scale)
         assert bool((w[ids < 0] == 0).all()) and int((ids < 0).sum()) >= 18
+
+
+SATURATED = [(8, 2, 1, 2), (8, 2, 2, 3), (64, 4, 2, 8), (96, 3, 1, 5), (96, 6, 3, 9), (60, 5, 2, 6), (256, 8, 4, 8), (130, 2, 1, 7),
+             (1024, 64, 5, 12)]
+
+
+@pytest.mark.parametrize("E,groups,top_groups,k", SATURATED)
+def test_scores_that_saturate(E, groups, top_groups, k):
+    """Sigmoid scores within 2^-53 of one, or of each other, in groups: without
+    a bias the order is that of the logits, and a group's that of the exact
+    sums, which such scores decide by what they lack of one."""
+    rng = np.random.default_rng(6)
+    kw = dict(score="sigmoid", groups=groups, top_groups=top_groups)
+    if E == 8:
+        ids, _ = check([[26, 26.5, 40, 45, 0, 0, 0, 0], [0, 0, 0, 0, 45, 40, 60, 50]], "f32", k, **kw)
+        assert ids[:, 0].tolist() == [3, 6]
+    for lo, hi in ((20, 60), (-60, -20), (36, 37), (-300, 300), (24.9, 25), (-700, 700)):
+        l = rng.uniform(lo, hi, size=(20, E))
+        check(l, "f32", k, **kw)
+        check(l, "bf16", k, renormalize=False, **kw)

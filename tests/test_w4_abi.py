@@ -250,3 +250,32 @@ def test_sizes_beyond_an_int():
         rs.lora_w4_apply_experts(None, wide, ids)
     with pytest.raises(ValueError, match="k is"):
         rs.lora_route(torch.zeros(1, 8), wrap + 2)
+
+
+def test_oracle_pair_order():
+    """Sums of two sigmoids in order, against 400-digit arithmetic, where
+    they differ by more than float64 rounds (2^-50 of the sum, or of what it
+    lacks of two)."""
+    import decimal
+
+    from oracle.w4_ref import pair_order
+
+    rng, seen = np.random.default_rng(8), 0
+    with decimal.localcontext() as ctx:
+        ctx.prec = 400
+
+        def exact(a, b):
+            return sum(1 / (1 + (-decimal.Decimal(v)).exp()) for v in (a, b))
+
+        for lo, hi in ((20, 60), (-60, -20), (-5, 5), (-300, 300), (40, 41)):
+            for _ in range(60):
+                p, q = rng.uniform(lo, hi, (2, 2)).astype(np.float32).astype(np.float64).tolist()
+                if exact(*p) < exact(*q):
+                    p, q = q, p
+                sp, sq = exact(*p), exact(*q)
+                if sp - sq > min(sq, 2 - sq) / 2**50:
+                    seen += 1
+                    assert pair_order(*p) > pair_order(*q), (p, q)
+    assert seen > 250
+    assert pair_order(-math.inf, 900.0) == pair_order(-math.inf, -math.inf) < pair_order(-800.0, -3e38)
+    assert pair_order(0.0, 0.0) == pair_order(1.0, -1.0) == (0, 1.0)
