@@ -173,6 +173,7 @@ void w4_rows_kernel(const W4RowsArgs p) {
   const int chunk = CHUNKED ? kChunk : p.k_tiles;
   const int plane = chunk * kW4K * 2, xrow_bytes = kParts * plane + 16;
   const int last_piece = p.d_in - 8;
+  const bool ragged = p.d_in % kW4K != 0;
   int e = 0, few_cnt = -1;
   bool none = false;
   if constexpr (kList) {
@@ -221,7 +222,7 @@ void w4_rows_kernel(const W4RowsArgs p) {
     };
     // ---- x into LDS, bf16: loads that write LDS directly, 64 pieces of 8
     // values (4 tiles) of one row each.  Pieces past d_in repeat the last
-    // one: they meet codes equal to their zero point, or a scale of 0.
+    // one, until clear_pads.
     auto dma_row = [&](char* dst, const char* src, int k0) {
       const int k = min(k0 + 8 * lane, last_piece);
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + (uint32_t)(2 * k)),
@@ -264,6 +265,21 @@ void w4_rows_kernel(const W4RowsArgs p) {
             for (int q = 0; q < kParts; ++q) *reinterpret_cast<uint4*>(lds + row * xrow_bytes + q * plane + 16 * at) = parts[q];
         }
       }
+    };
+
+    // The last tile's pieces past d_in, at tile `kt` of x's rows in LDS, become
+    // zeros once x is there: whatever their codes and scales, they then add
+    // nothing, to sums near the largest float32 either.  (A choice of address
+    // in the loads made 23 rows 18944 -> 3584 21.4 us a call, against 16.9; here
+    // only a d_in that ends inside a tile pays, one barrier.)
+    auto clear_pads = [&](char* dst, int kt) {
+      const int piece = tid & 15;
+      if (piece >= (p.d_in % kW4K) / 8)
+        for (int row = tid >> 4; row < x_rows; row += 4 * W)
+#pragma unroll
+          for (int q = 0; q < kParts; ++q)
+            *reinterpret_cast<uint4*>(dst + row * xrow_bytes + q * plane + kt * kW4K * 2 + 16 * piece) = make_uint4(0u, 0u, 0u, 0u);
+      lds_barrier();
     };
 
     // ---- codes: U tiles of each output block in flight per wave, taken in
@@ -393,6 +409,7 @@ void w4_rows_kernel(const W4RowsArgs p) {
           part_rows(c0);
         }
         lds_barrier();
+        if (ragged && c0 + kChunk >= p.k_tiles) clear_pads(lds + at, p.k_tiles - 1 - c0);
         run(lds + at, lds + (buf - at), c0, min(t_end, c0 + kChunk), c0 + kChunk < t_end);
         at = buf - at;
       }
@@ -400,6 +417,7 @@ void w4_rows_kernel(const W4RowsArgs p) {
       if constexpr (kDma) wait_loads<kCodeLoads>();
       else part_rows(0);
       lds_barrier();
+      if (ragged) clear_pads(lds, p.k_tiles - 1);
       run(lds, lds, t_begin, t_end, false);
     }
 

@@ -580,3 +580,35 @@ def test_refused_on_the_gpu():
         rs.lora_w4_apply_experts(st, x, ids, None, torch.zeros(4, 16, dtype=torch.bfloat16, device=dev))
     with pytest.raises(rs.LoraError):
         rs.lora_w4_apply_experts(st, torch.zeros(4, 68, dtype=torch.bfloat16, device=dev)[:, 2:66], ids)
+
+
+# rows, d_in: one piece of 8 inputs, a last tile with one or nine, in one go and in chunks
+@pytest.mark.parametrize("T,d_in", [(1, 8), (1, 136), (3, 200), (17, 136), (40, 136), (9, 4104), (16, 5128), (40, 4104)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_large_values_in_the_last_inputs(T, d_in, group, dtype):
+    """The last tile's inputs alone count, at sums of |x| up to what lora.h
+    states for bf16 (2^122 in a group), and where the formula ends for float32
+    (15 |x| below 2^128)."""
+    dev = device()
+    note(f"w4 large {T} {d_in} {group} {dtype}")
+    d_out = 40
+    packed, s, z = make(140, 1, d_out, d_in, group, True, "bf16")
+    s = np.exp2(np.round(np.log2(s)) - 20).astype(np.float32)
+    x = acts(141, T, d_in, "bf16").astype(np.float64)
+    x[:, d_in - 8:] = np.random.default_rng(142).choice([-1.0, 1.0, 0.5], (T, 8)) * 2.0 ** 118
+    if dtype == "f32":
+        x[:, d_in - 8:] = 0.0
+        x[np.arange(T), d_in - 1 - np.arange(T) % 8] = 2.0 ** 123  # one input of a row: 15 |x| < 2^127
+    x = x.astype(np.float32)
+    st = pack(packed, s, z, group, "bf16", dev)
+    y = rs.lora_w4_apply(st, torch.from_numpy(x).to(dev).to(DT[dtype]))
+    a = (packed[0], s[0], z[0], group, x)
+    assert_close(y, w4_apply_ref(*a), w4_magnitude_ref(*a), d_in, group, dtype)
+    ids = torch.arange(T, dtype=torch.int32, device=dev).remainder(2).sub(1).abs().sub(1).unsqueeze(1).contiguous()  # 0, -1, 0, ...
+    w = torch.full((T, 1), 0.5, device=dev)
+    y = rs.lora_w4_apply_experts(st, torch.from_numpy(x).to(dev).to(DT[dtype]), ids, w)
+    ref, mag = 0.5 * w4_apply_ref(*a), 0.5 * w4_magnitude_ref(*a)
+    hole = ids.cpu().numpy()[:, 0] < 0
+    ref[hole], mag[hole] = 0, 0
+    assert_close(y, ref, mag, d_in, group, dtype, k=1)
