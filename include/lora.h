@@ -670,7 +670,10 @@ int lora_w4_apply(const lora_w4_store* store_host, int dtype, const void* x, int
  *   weights      : NULL: y has T k rows, y[t k + j] = W_{ids[t, j]} x;
  *                  float32 [T, k]: y has T rows,
  *                  y[t] = sum_j weights[t, j] W_{ids[t, j]} x, summed in
- *                  float32 in a fixed order and rounded once.
+ *                  float32 in a fixed order and rounded once (the weight
+ *                  multiplies a matrix's row, or for few rows its groups'
+ *                  sums).  A weight that is infinite or NaN gives a row
+ *                  without finite values.
  * An id outside [0, n) names no matrix: its row of y is zero, and it adds
  * nothing to a sum whatever its weight (a token without any gets a row of
  * zeros), whatever its x row holds.  The same id may appear twice in a token.

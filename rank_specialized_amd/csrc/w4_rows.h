@@ -348,7 +348,7 @@ void w4_rows_kernel(const W4RowsArgs p) {
 #pragma unroll
         for (int a = 0; a < RT; ++a) {
           const uint32_t cw[4] = {code[u][a].x, code[u][a].y, code[u][a].z, code[u][a].w};
-          const float sc = kSumUp ? par[u][a].scale(s) * slot_w[u] : par[u][a].scale(s);
+          const float sc = par[u][a].scale(s);
           const float z32 = par[u][a].zero32(s);
           uint4 b[kSteps];
 #pragma unroll
@@ -364,7 +364,10 @@ void w4_rows_kernel(const W4RowsArgs p) {
 #pragma unroll
               for (int q = 0; q < kParts; ++q) c = mfma_bf16_16x16x32(xp[t][j][q], b[j], c);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) acc[a][t][v] = fmaf(sc, c[v], acc[a][t][v]);
+            for (int v = 0; v < 4; ++v)
+              // The weight multiplies what the scale gave: their own product
+              // need not be a number that float32 holds.
+              acc[a][t][v] = kSumUp ? fmaf(slot_w[u], sc * c[v], acc[a][t][v]) : fmaf(sc, c[v], acc[a][t][v]);
           }
         }
       }

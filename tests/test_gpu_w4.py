@@ -612,3 +612,41 @@ def test_large_values_in_the_last_inputs(T, d_in, group, dtype):
     hole = ids.cpu().numpy()[:, 0] < 0
     ref[hole], mag[hole] = 0, 0
     assert_close(y, ref, mag, d_in, group, dtype, k=1)
+
+
+@pytest.mark.parametrize("T,k", [(1, 4), (3, 2), (40, 4), (300, 2)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("by_scale,by_weight,by_x", [(-80, -75, 100), (90, 70, -100), (-30, -120, 60), (30, 100, -60)])
+def test_scale_times_weight_out_of_range(T, k, dtype, by_scale, by_weight, by_x):
+    """Scales and weights whose products no float32 holds, rows that do."""
+    dev = device()
+    note(f"w4 weight {T} {k} {dtype} {by_scale}")
+    E, d_in, d_out, group = 5, 264, 40, 64
+    packed, s, z, x, ids, w = experts_case((T, k, E, d_in, d_out, group, True, "f32", dtype, False, True), 150, dev)
+    s, w, x = (np.ldexp(v, e).astype(np.float32) for v, e in ((s, by_scale), (w, by_weight), (x, by_x)))
+    st = pack(packed, s, z, group, "f32", dev)
+    y = rs.lora_w4_apply_experts(st, torch.from_numpy(x).to(dev).to(DT[dtype]), torch.from_numpy(ids).to(dev),
+                                 torch.from_numpy(w).to(dev))
+    ref = experts_ref(packed, s, z, group, x, ids, w)
+    mag = experts_ref(packed, s, z, group, x, ids, w, product=w4_magnitude_ref)
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24  # tolerance() has 1e-30 in it: as large as these values
+    tol = half * np.abs(ref) * (1 + 2.0 ** -8) + (64 + 5 + 32 + k + 2) * 2.0 ** -23 * mag
+    assert np.isfinite(host(y)).all() and (np.abs(host(y) - ref) <= tol).all()
+    assert np.abs(ref).max() > 0
+
+
+@pytest.mark.parametrize("T", [1, 12, 300])
+def test_weights_that_are_not_finite(T):
+    """No finite value in such a token's row; the other tokens keep theirs."""
+    dev = device()
+    packed, s, z, x, ids, w = experts_case((T, 2, 4, 264, 40, 64, True, "bf16", "bf16", False, True), 160, dev, hole=False)
+    st = pack(packed, s, z, 64, "bf16", dev)
+    xd, idd, wd = torch.from_numpy(x).to(dev).bfloat16(), torch.from_numpy(ids).to(dev), torch.from_numpy(w).to(dev)
+    good = rs.lora_w4_apply_experts(st, xd, idd, wd)
+    for bad in (float("inf"), float("nan")):
+        wb = wd.clone()
+        wb[T // 2, 1] = bad
+        y = rs.lora_w4_apply_experts(st, xd, idd, wb)
+        keep = [t for t in range(T) if t != T // 2]
+        assert np.array_equal(hbits(y[keep]), hbits(good[keep]))
+        assert not bool(torch.isfinite(y[T // 2]).any())
