@@ -680,6 +680,15 @@ def _ld(t: torch.Tensor, name: str) -> int:
     return ld if rows > 1 else cols
 
 
+def _scratch(ws: torch.Tensor) -> int:
+    """Bytes of a workspace tensor: all of them one run of memory, so that
+    its size says how far a kernel may write (that of an expanded tensor or of
+    a strided view does not)."""
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.numel() * ws.element_size()
+
+
 def _dtype(t: torch.Tensor, name: str) -> int:
     dt = _DTYPES.get(t.dtype)
     if dt is None:
@@ -764,8 +773,7 @@ def _w4_run(name: str, store: W4Store, x: torch.Tensor, rows: int, y, T: int, k:
         ws_ptr = ws.data_ptr() if nb else None
     else:
         _same_device(index, ws=ws)
-        nb = ws.numel() * ws.element_size()
-        ws_ptr = _p(ws)
+        nb, ws_ptr = _scratch(ws), _p(ws)
     _call(name, index, store._ref, dt, _p(x), ldx, *middle[0], _p(y), ldy, T, *middle[1], ws_ptr, nb)
     return y
 

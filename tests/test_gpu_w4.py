@@ -650,3 +650,19 @@ def test_weights_that_are_not_finite(T):
         keep = [t for t in range(T) if t != T // 2]
         assert np.array_equal(hbits(y[keep]), hbits(good[keep]))
         assert not bool(torch.isfinite(y[T // 2]).any())
+
+
+def test_workspace_refused_on_the_gpu():
+    """The calls check it before anything is launched."""
+    dev = device()
+    packed, s, z = make(170, 2, 16, 64, 32, False, "bf16")
+    st = pack(packed, s, z, 32, "bf16", dev)
+    x, ids = torch.zeros(400, 64, dtype=torch.bfloat16, device=dev), torch.zeros(400, 2, dtype=torch.int32, device=dev)
+    need = rs.lora_w4_workspace_bytes(st, torch.bfloat16, 400, 2)
+    assert need > 0
+    for bad in (torch.zeros(1, dtype=torch.uint8, device=dev).expand(need), torch.zeros(2 * need, dtype=torch.uint8, device=dev)[::2]):
+        with pytest.raises(ValueError, match="ws must be contiguous"):
+            rs.lora_w4_apply_experts(st, x, ids, ws=bad)
+    with pytest.raises(rs.LoraError):
+        rs.lora_w4_apply_experts(st, x, ids, ws=torch.zeros(need - 1, dtype=torch.uint8, device=dev))
+    rs.lora_w4_apply_experts(st, x, ids, ws=torch.zeros(need, dtype=torch.uint8, device=dev))

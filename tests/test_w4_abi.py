@@ -279,3 +279,13 @@ def test_oracle_pair_order():
     assert seen > 250
     assert pair_order(-math.inf, 900.0) == pair_order(-math.inf, -math.inf) < pair_order(-800.0, -3e38)
     assert pair_order(0.0, 0.0) == pair_order(1.0, -1.0) == (0, 1.0)
+
+
+def test_workspace_is_one_run_of_memory():
+    """An expanded tensor or a strided view has more bytes by its shape than
+    there are behind its address."""
+    one = torch.zeros(1, dtype=torch.uint8)
+    for bad in (one.expand(1 << 20), torch.zeros(64, 64)[:, ::2], torch.zeros(8, 16).t()):
+        with pytest.raises(ValueError, match="contiguous"):
+            rs._scratch(bad)
+    assert rs._scratch(torch.zeros(64, 8)) == 2048 and rs._scratch(torch.zeros(64, 8)[8:24]) == 512
