@@ -1,13 +1,15 @@
 // Host-side helpers of the launchers: the current device, device attributes
 // cached per device, and the dynamic-LDS attribute of a kernel raised once
 // per (kernel, device).  Every cache is an array of atomics indexed by the
-// device, so concurrent calls from several host threads, on one device or on
-// several, share no unsynchronized state.
+// device, raised under a lock where the device's own state goes with it, so
+// concurrent calls from several host threads, on one device or on several,
+// share no unsynchronized state.
 #pragma once
 #include <hip/hip_runtime.h>
 
 #include <atomic>
 #include <cstddef>
+#include <mutex>
 
 namespace lora {
 
@@ -52,23 +54,24 @@ inline int cu_count() {
 // object per kernel (a function-local static of its launcher).
 struct DynLdsLimit {
   std::atomic<size_t> raised[kMaxDevices];
+  std::mutex raising;
 };
 
 // Allow `fn` `lds` bytes of dynamic LDS on the current device (above 48 KiB
-// the attribute must be set).  Two threads racing here both set the
-// attribute, which is idempotent, and the recorded limit only grows.
+// the attribute must be set).  One thread at a time sets it: of two that ask
+// for different sizes the smaller must not be the last, while the record says
+// the larger.
 inline hipError_t ensure_dynamic_lds(DynLdsLimit& lim, const void* fn, size_t lds) {
   if (lds <= 48 * 1024) return hipSuccess;
   int dev = 0;
   hipError_t e = current_device(&dev);
   if (e != hipSuccess) return e;
-  size_t cur = lim.raised[dev].load(std::memory_order_acquire);
-  if (lds <= cur) return hipSuccess;
+  if (lds <= lim.raised[dev].load(std::memory_order_acquire)) return hipSuccess;
+  const std::lock_guard<std::mutex> one(lim.raising);
+  if (lds <= lim.raised[dev].load(std::memory_order_relaxed)) return hipSuccess;
   e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-  if (e != hipSuccess) return e;
-  while (cur < lds && !lim.raised[dev].compare_exchange_weak(cur, lds, std::memory_order_acq_rel)) {
-  }
-  return hipSuccess;
+  if (e == hipSuccess) lim.raised[dev].store(lds, std::memory_order_release);
+  return e;
 }
 
 }  // namespace lora
