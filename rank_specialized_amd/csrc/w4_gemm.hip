@@ -390,8 +390,9 @@ void w4_gemm_kernel(const W4GemmArgs p) {
   for (int kt = k0; kt < k1; ++kt) {
     const bool more = kt + 1 < k1;
     // This step's x and codes were asked for a whole step ago; every wave has
-    // finished with the buffer that is filled next.
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    // finished with the buffer that is filled next: its reads of it have ended
+    // (lgkmcnt), which the barrier itself does not wait for.
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     uint4 b[kRT][4];
