@@ -666,3 +666,58 @@ def test_workspace_refused_on_the_gpu():
     with pytest.raises(rs.LoraError):
         rs.lora_w4_apply_experts(st, x, ids, ws=torch.zeros(need - 1, dtype=torch.uint8, device=dev))
     rs.lora_w4_apply_experts(st, x, ids, ws=torch.zeros(need, dtype=torch.uint8, device=dev))
+
+
+def one_input(T, d_in, d_out, group, seed=180):
+    """Float32 rows with one input each, of 24 significant bits, codes a power
+    of two from their zero points, scales powers of two: y is exact, and holds
+    every bit of that input."""
+    rng = np.random.default_rng(seed)
+    packed, s, z = make(seed, 1, d_out, d_in, group, True, "f32")
+    s = np.exp2(rng.integers(-3, 4, s.shape)).astype(np.float32)
+    z = rng.integers(0, 8, z.shape).astype(np.uint8)
+    step = rng.choice([1, 2, 4, 8], (1, d_out, d_in))
+    q = z.repeat(group, -1)[..., :d_in] + np.where(step <= z.repeat(group, -1)[..., :d_in], rng.choice([-1, 1], step.shape), 1) * step
+    assert q.min() >= 0 and q.max() <= 15
+    packed = (q[..., 0::2] | (q[..., 1::2] << 4)).astype(np.uint8)
+    x = np.zeros((T, d_in), np.float32)
+    odd = rng.integers(2 ** 23, 2 ** 24, T) | 1  # all 24 bits from the first to the last
+    x[np.arange(T), rng.integers(0, d_in, T)] = (odd * np.exp2(rng.integers(-40, 20, T).astype(float)) * rng.choice([-1, 1], T))
+    return packed, s, z, x
+
+
+@pytest.mark.parametrize("T,d_in,d_out,group", [(1, 520, 72, 32), (5, 4104, 40, 128), (17, 1032, 136, 64), (40, 264, 40, 32),
+                                                (33, 5128, 24, 96), (300, 136, 24, 64)])
+def test_float32_rows_are_whole(T, d_in, d_out, group):
+    """Each of the three bf16 parts of x counts (test_w4_abi.py: without the
+    last, no row would be right), for rows and for weighted sums."""
+    dev = device()
+    note(f"w4 whole float32 {T} {d_in} {group}")
+    packed, s, z, x = one_input(T, d_in, d_out, group)
+    st = pack(packed, s, z, group, "f32", dev)
+    xd = torch.from_numpy(x).to(dev)
+    ref = w4_apply_ref(packed[0], s[0], z[0], group, x)
+    assert np.array_equal(ref, ref.astype(np.float32))
+    assert np.array_equal(host(rs.lora_w4_apply(st, xd)), ref)
+    ids = torch.zeros(T, 2, dtype=torch.int32, device=dev)
+    ids[:, 1] = 1  # there is no such matrix
+    y = rs.lora_w4_apply_experts(st, xd, ids, torch.full((T, 2), -0.5, device=dev))
+    assert np.array_equal(host(y), -0.5 * ref)
+    assert np.array_equal(host(rs.lora_w4_apply_experts(st, xd, ids)[::2]), ref)
+
+
+def test_passes_in_turn_repeat():
+    """Calls that nothing waits between, of several sizes and inputs in turn:
+    each gives the bits of its first."""
+    dev = device()
+    jobs = []
+    for i, (T, d_in, d_out, group) in enumerate([(1, 3584, 512, 128), (1, 1000, 2056, 64), (23, 3592, 520, 64), (7, 520, 136, 32)]):
+        packed, s, z = make(190 + i, 1, d_out, d_in, group, i > 0, "bf16")
+        st = pack(packed, s, z, group, "bf16", dev)
+        jobs += [(st, torch.from_numpy(acts(195 + 2 * i + j, T, d_in, "bf16")).to(dev).bfloat16()) for j in range(2)]
+    first = [rs.lora_w4_apply(st, x) for st, x in jobs]
+    torch.cuda.synchronize()
+    turns = [[rs.lora_w4_apply(st, x) for st, x in jobs] for _ in range(60)]
+    for ys in turns:
+        for y, want in zip(ys, first):
+            assert torch.equal(y.view(torch.int16), want.view(torch.int16))

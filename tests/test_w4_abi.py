@@ -289,3 +289,21 @@ def test_workspace_is_one_run_of_memory():
         with pytest.raises(ValueError, match="contiguous"):
             rs._scratch(bad)
     assert rs._scratch(torch.zeros(64, 8)) == 2048 and rs._scratch(torch.zeros(64, 8)[8:24]) == 512
+
+
+def test_float32_inputs_need_all_parts():
+    """The inputs of the GPU's test of whole float32 rows tell three bf16 parts
+    of x from two, in the oracle's product."""
+    from test_gpu_w4 import one_input
+
+    def part(v):
+        return (v.view(np.uint32) & np.uint32(0xFFFF0000)).view(np.float32)
+
+    for T, d_in, d_out, group in ((5, 4104, 40, 128), (300, 136, 24, 64)):
+        packed, s, z, x = one_input(T, d_in, d_out, group)
+        hi = part(x)
+        mid = part(x - hi)
+        assert np.array_equal(hi + mid + (x - hi - mid), x) and ((x - hi - mid).any(1)).all()
+        whole = w4_apply_ref(packed[0], s[0], z[0], group, x)
+        assert (whole != 0).all()
+        assert (w4_apply_ref(packed[0], s[0], z[0], group, hi + mid) != whole).all()
