@@ -614,6 +614,8 @@ class W4Store:
         c = self.c
         self.n, self.d_in, self.d_out, self.group = c.n, c.d_in, c.d_out, c.group
         self.device_index = self.codes.get_device()
+        if self.device_index < 0 or self.params.get_device() != self.device_index:
+            raise ValueError("codes and params must be on one GPU")
         self._ref = C.byref(c)
         self._ws_bytes = {}
 

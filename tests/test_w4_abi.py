@@ -307,3 +307,13 @@ def test_float32_inputs_need_all_parts():
         whole = w4_apply_ref(packed[0], s[0], z[0], group, x)
         assert (whole != 0).all()
         assert (w4_apply_ref(packed[0], s[0], z[0], group, hi + mid) != whole).all()
+
+
+def test_store_is_on_a_gpu():
+    """Buffers moved to the host would pass for those of x on the host, and
+    the kernels would be given host addresses."""
+    b = torch.zeros(2048, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU"):
+        rs.W4Store(store(), b, b)
+    with pytest.raises(ValueError, match="GPU"):
+        rs.W4Store(store(), b.to("meta"), b.to("meta"))
