@@ -577,9 +577,10 @@ int lora_rsvd_factor_phases(int n, int d_in, int d_out, int dtype, int r, const 
 
 /*
  * 4-bit base layers.  The layers that adapters are added to are often held as
- * 4-bit codes with a scale (and a zero point) per group of inputs ("Compress
- * then Serve" section 10 trains its adapters on a 4-bit base).  A w4 store
- * holds n matrices of one shape, matrix e being
+ * 4-bit codes.  Those held here are affine, a scale (and a zero point) per
+ * group of inputs.  ("Compress then Serve" section 10 trains its adapters on
+ * a 4-bit base too, but one of NF4, a codebook of 16 values that s (q - z)
+ * does not hold.)  A w4 store holds n matrices of one shape, matrix e being
  *
  *     W_e[o, k] = s_e[o, g] * (q_e[o, k] - z_e[o, g])      g = k / group
  *
@@ -603,7 +604,11 @@ typedef struct lora_w4_store {
 } lora_w4_store;
 
 /* Most matrices of a store, largest d_in and d_out, and most rows (T, or
- * T * k) of a call. */
+ * T * k) of a call.  Rows are taken at a prefill kernel's rate where they are
+ * bf16 and, as float16 padded to a multiple of 128 inputs, T or T * k of them
+ * (also where choices share a row) stay below 2^32 bytes, a matrix's codes
+ * below 2^31.  Otherwise the codes are read and expanded again for every 64
+ * rows (float32: 32). */
 #define LORA_W4_MAX_N 1024
 #define LORA_W4_MAX_DIM (1 << 20)
 #define LORA_W4_MAX_ROWS (1 << 20)
@@ -635,8 +640,9 @@ int lora_w4_pack(lora_w4_store* out_host, int n, int d_in, int d_out, int group,
 /*
  * Workspace of lora_w4_apply (k = 0) and of lora_w4_apply_experts (k >= 1;
  * weighted: whether weights are given) for T tokens of this dtype (host only;
- * 0 when none is needed, and on invalid arguments).  Scratch: no
- * initialization, and not shared by calls in flight together.
+ * 0 when none is needed, and on invalid arguments).  T k rows of x are
+ * counted also where a token's choices share one (the query does not say).
+ * Scratch: no initialization, and not shared by calls in flight together.
  */
 size_t lora_w4_workspace_bytes(const lora_w4_store* store_host, int dtype, int T, int k, int weighted);
 
@@ -650,11 +656,16 @@ size_t lora_w4_workspace_bytes(const lora_w4_store* store_host, int dtype, int T
  * q - z is an integer that bf16 holds, so every product is exact in float32;
  * they are summed in float32 within a group, the groups' sums times their
  * scales in float32, and y rounds once.  Float32 x is taken in whole (as
- * three bf16 parts).  Results do not change from call to call.  A row of x
- * with an infinity or a NaN gives a row of y without finite values; other
- * rows are not touched by it.  (bf16 rows of few are multiplied with 32 + q
- * and the excess taken off: a group whose |x| sum to more than 2^122 may
- * overflow where the formula does not.)  Enqueues one to three kernels.
+ * three bf16 parts; bits below 2^-133 are dropped).  Results do not change
+ * from call to call.  A row of x with an infinity or a NaN gives a row of y
+ * without finite values; other rows are not touched by it.
+ *   Few bf16 rows are multiplied with 32 + q and the excess taken off: a
+ * group whose |x| sum to more than 2^122 may overflow where the formula does
+ * not.  Many are multiplied as float16, each row times the power of two that
+ * brings its largest value to 2^14 or just above: values below 2^-31 of that
+ * largest are rounded, by at most 2^-39 of it, and a row of W whose |W| sum
+ * to more than 2^113 may overflow where the formula does not.
+ *   Enqueues one to three kernels.
  * Errors: INVALID_ARG (null pointers, T < 0, ldx < d_in, ldy < d_out, a store
  * of several matrices, ws too small); UNSUPPORTED (sizes as lora_w4_bytes,
  * alignment, T above LORA_W4_MAX_ROWS).

@@ -721,3 +721,24 @@ def test_passes_in_turn_repeat():
     for ys in turns:
         for y, want in zip(ys, first):
             assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
+FEW = [(1, 136, 40), (17, 520, 72), (40, 136, 40)]
+
+
+@pytest.mark.parametrize("T,d_in,d_out,dtype,unit", [
+    *[(*f, dtype, unit) for f in FEW for dtype, unit in (("bf16", -133), ("bf16", -126), ("f32", -133), ("f32", -126), ("f32", -112))],
+    (301, 1032, 8200, "bf16", -133), (301, 1032, 8200, "bf16", -126)])
+def test_smallest_values(T, d_in, d_out, dtype, unit):
+    """x of a few of the smallest steps that lora.h says are kept, and near the
+    smallest normal numbers, on large scales: exact."""
+    dev = device()
+    note(f"w4 smallest {T} {dtype} {unit}")
+    packed, s, z = make(260, 1, d_out, d_in, 64, True, "bf16")
+    s = np.exp2(np.random.default_rng(261).integers(98, 102, s.shape)).astype(np.float32)
+    x = np.ldexp(np.random.default_rng(262).integers(-4, 5, (T, d_in)).astype(np.float64), unit)
+    assert np.array_equal(x, x.astype(np.float32))
+    x = x.astype(np.float32)
+    y = rs.lora_w4_apply(pack(packed, s, z, 64, "bf16", dev), torch.from_numpy(x).to(dev).to(DT[dtype]))
+    want = torch.from_numpy(w4_apply_ref(packed[0], s[0], z[0], 64, x)).to(DT[dtype])
+    assert np.array_equal(host(y), host(want))

@@ -205,3 +205,17 @@ def test_experts_captured(case):
         torch.cuda.synchronize()
         for o in outs:
             assert np.array_equal(hbits(o), hbits(want)), i
+
+
+@pytest.mark.parametrize("by", [-120, 80, 97])
+@pytest.mark.parametrize("T,d_in,d_out,bm,splits", [DENSE[0], DENSE[3]])
+def test_scales_at_their_bounds(T, d_in, d_out, bm, splits, by):
+    """Rows of W that sum to up to the 2^113 that lora.h states; small ones."""
+    dev = device()
+    note(f"w4 scales {T} {d_in} 2^{by}")
+    packed, s, z = whole(270, 1, d_out, d_in, 64, True)
+    s = np.ldexp(s, by).astype(np.float32)
+    assert np.abs(w4_matrix_ref(packed[0], s[0], z[0], 64)).sum(1).max() < 2.0 ** 113
+    x = integers(271, T, d_in)
+    y = rs.lora_w4_apply(pack(packed, s, z, 64, "bf16", dev), torch.from_numpy(x).to(dev).to(BF16))
+    assert np.array_equal(hbits(y), rounded(w4_apply_ref(packed[0], s[0], z[0], 64, x)))
