@@ -270,15 +270,18 @@ void w4_rows_kernel(const W4RowsArgs p) {
     // The last tile's pieces past d_in, at tile `kt` of x's rows in LDS, become
     // zeros once x is there: whatever their codes and scales, they then add
     // nothing, to sums near the largest float32 either.  (A choice of address
-    // in the loads made 23 rows 18944 -> 3584 21.4 us a call, against 16.9; here
+    // in the loads made 23 rows 18944 -> 3584 21.4 us a call, against 17.2; here
     // only a d_in that ends inside a tile pays, one barrier.)
     auto clear_pads = [&](char* dst, int kt) {
-      const int piece = tid & 15;
-      if (piece >= (p.d_in % kW4K) / 8)
-        for (int row = tid >> 4; row < x_rows; row += 4 * W)
+      int id = (int)threadIdx.x;
+      asm volatile("" : "+v"(id));  // nothing of this is formed before, to hold registers
+      const int pads = (kW4K - p.d_in % kW4K) / 2;  // dwords
+#pragma unroll 1
+      for (int row = id >> 6; row < x_rows; row += W)
 #pragma unroll
-          for (int q = 0; q < kParts; ++q)
-            *reinterpret_cast<uint4*>(dst + row * xrow_bytes + q * plane + kt * kW4K * 2 + 16 * piece) = make_uint4(0u, 0u, 0u, 0u);
+        for (int q = 0; q < kParts; ++q)
+          if ((id & 63) < pads)
+            reinterpret_cast<uint32_t*>(dst + row * xrow_bytes + q * plane + (kt + 1) * kW4K * 2)[-1 - (id & 63)] = 0u;
       lds_barrier();
     };
 
