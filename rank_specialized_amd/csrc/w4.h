@@ -90,9 +90,11 @@ inline int64_t w4_max_tiles(int R, int n, int bm) { return plan_max_runs(R, n + 
 // with a compute unit each; a workgroup's time goes with its tiles of inputs;
 // splits have their float32 rows written, read and added.  The constants are
 // fitted to times measured at 200 to 6000 rows of 4096 -> 14336, 14336 -> 4096,
-// 4096 -> 4096 and 1368 -> 4888 (with groups of 128; of 64 they come 3% to 10%
-// larger), which they give to 5%.  Whole rounds matter: 1024 rows of 4096 ->
-// 4096 52 us with tiles of 64 rows, 67 with 96; 2481 rows 107 and 87.
+// 4096 -> 4096 and 1368 -> 4888 with groups of 128, which they give to 5%.
+// Groups of 64 come 3% to 25% larger and of 32 25% to 40% (8192 rows of 4096 ->
+// 14336 1091 and 1180 us, where groups of 128 took 917 in that run); the choice
+// between the tiles was not fitted there.  Whole rounds matter: 1024 rows of
+// 4096 -> 4096 52 us with tiles of 64 rows, 67 with 96; 2481 rows 107 and 87.
 inline double w4_many_us(int rows, int64_t tiles, int per_split, int splits, double outputs) {
   const int64_t groups = tiles * splits, full = groups / 512, rest = groups % 512;
   const double pair = rows == kW4BigTile ? 2.23 : 1.72, alone = rows == kW4BigTile ? 1.66 : 1.15;

@@ -6,9 +6,15 @@
 // 16 NT rows x 256 outputs, each of its waves 32 or 64 outputs of all the rows,
 // so that a code is unpacked once per 16 NT rows; the waves share the rows of x
 // in LDS, staged 128 inputs at a time by loads that write LDS directly, two
-// buffers.  Measured: 8192 rows 4096 -> 14336 805 to 870 us with the GPU's clock
-// (1.1 to 1.2 PFLOP/s; a library's bf16 product of that shape 722) and 27 for
-// the rows as f16; 32 experts of 512 rows 2048 -> 2816 222 us (0.85).
+// buffers.  Measured: 8192 rows 4096 -> 14336 775 to 800 us in long runs (1.2
+// PFLOP/s; a library's bf16 product of that shape 712), 770 to 1080 by the
+// clock in traces of a few, and 27 for the rows as f16; 32 experts of 512 rows
+// 2048 -> 2816 207 us (0.9).
+//
+// By matrix the grid is that of the most tiles there can be, and each XCD has
+// an eighth of it: the tiles that do not exist are all the last XCDs' (191 of
+// 203 tiles in the case above, where the busiest has 7% more than the mean).  A
+// tile of fewer rows costs a whole one.
 //
 // The codes enter the products as f16 numbers: 256 + q or 16 + q (the two
 // places of a code in f16's ten fraction bits, so that one shift serves four
@@ -225,9 +231,11 @@ constexpr int kCols = 256;  // outputs of a workgroup
 // Its waves, each with kCols / waves of the outputs.  Eight waves of two
 // 16-output blocks fit four to a SIMD, four waves of four blocks two; with
 // more than one scale per tile and output eight no longer fit their
-// registers.  Measured (8, 4 waves): 32 experts of 512 rows 2048 -> 2816 222,
-// 238 us; 8192 rows 4096 -> 14336 805 to 925, 848, with groups of 64 and zero
-// points 1019, 1007, of 32 1316, 1153.
+// registers.  Measured side by side (8, 4 waves): 32 experts of 512 rows 2048
+// -> 2816 222, 238 us; with groups of 64 and zero points 8192 rows 4096 ->
+// 14336 1019, 1007, of 32 1316, 1153.  With four waves, four float32 scales per
+// tile and output spill 29 to 31 registers at 96 rows (4 at 64), every other
+// form at most 2.
 constexpr int gemm_waves(int sub) { return sub == 1 ? 8 : 4; }
 constexpr int kTileOrder = 4;  // row tiles walked together (w4_tile_of)
 

@@ -18,10 +18,10 @@
 // through the load path: 19.0 us for one token, 3584 -> 18944, against 9.3.)
 //
 // Measured (kernel times, three sets of weights in turn): one token 3584 ->
-// 18944 9.3 us (35.6 MB, 3.8 TB/s); 23 rows 18944 -> 3584 in groups of 64 14.0
-// (2.7) and 4.0 for the splits' sum; one token's eight experts of 64, 2048 ->
-// 2816, 7.9 (23.8 MB, 3.0), eight tokens' 28.7 (about 120 MB, 4.2); 180 rows
-// of 32 experts 1408 -> 2048 in groups of 32 18.0 (2.9): with few bytes the
+// 18944 9.3 to 9.7 us (35.6 MB, 3.7 TB/s); 23 rows 18944 -> 3584 in groups of
+// 64 14.6 (2.6) and 3.9 for the splits' sum; one token's eight experts of 64,
+// 2048 -> 2816, 8.1 (23.8 MB, 2.9), eight tokens' 28.7 (about 120 MB, 4.2); 180 rows
+// of 32 experts 1408 -> 2048 in groups of 32 18.2 (2.9): with few bytes the
 // launch, the copy of x and the last sums show, with fine groups the
 // instructions per code.  The codes' loads go through the caches (past them,
 // as data read once, one token took 10.4, the 23 rows 16.2).  More waves in a
@@ -138,9 +138,10 @@ __device__ __forceinline__ void wait_loads() {
 enum Mode { kRun, kListed, kSum };
 
 // x in LDS.  Not CHUNKED: all of the rows' inputs.  CHUNKED: kChunk tiles of
-// 16 NT rows; of 16 bf16 rows two such buffers, filled in turn (with more rows
-// a second buffer costs the workgroups that would hide the loads: 64 rows
-// 3584 -> 3584 13.7 us with two, 10.7 with one).
+// 16 NT rows; of 16 bf16 rows two such buffers, filled in turn.  More rows
+// have one, which every chunk waits for with the codes in flight: of 64 rows a
+// second costs the workgroups that would hide the loads (3584 -> 3584 13.7 us
+// with two, 10.7 with one); of 32 it was not measured.
 constexpr int kChunk = 4;
 template <typename E, int NT, bool CHUNKED>
 constexpr int x_buffers() {
