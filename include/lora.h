@@ -717,8 +717,8 @@ int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void
  * weight 0.  A group with fewer than two experts that can be chosen comes
  * after every other in the sigmoid form (if it has two or more).
  * Without a bias the order of c is that of the logits, whatever a score
- * rounds to; a group's sum of two is compared in float64 where it is at most
- * one and by what it lacks of two above.  With a bias c is formed in float64,
+ * rounds to; a group's sum of two is compared in float64, near one and two as
+ * its distance from there.  With a bias c is formed in float64,
  * and what is equal there is a tie: sigmoid scores of logits above 36.7 that
  * have one bias, scores below 2^-53 of theirs.
  *   logits [T, ldl] : dtype rows, ldl >= E, naturally aligned (no 16-byte

@@ -69,14 +69,18 @@ def experts_ref(packed, scales, zeros, group: int, x, ids, weights=None, product
 
 def pair_order(a: float, b: float):
     """A key that orders as sigmoid(a) + sigmoid(b) does; -inf stands for no
-    logit, and sums without two come first.  A sum above one is its distance
-    from two, which a float holds where 1 - 2^-60 is not one."""
-    def sig(v):
-        return math.exp(v) / (1 + math.exp(v)) if v < 0 else 1 / (1 + math.exp(-v))
-
-    if min(a, b) == -math.inf:
+    logit, and sums without two come first.  The sum is held as it is, or as
+    its distance from one or two where it is near them, which a float holds
+    where 1 - 2^-60 is not one."""
+    hi, lo = max(a, b), min(a, b)
+    if lo == -math.inf:
         return (-1, 0.0)
-    return (1, -(sig(-a) + sig(-b))) if a + b > 0 else (0, sig(a) + sig(b))
+    p, q = (math.exp(-abs(v)) / (1 + math.exp(-abs(v))) for v in (hi, lo))
+    if hi <= 0:
+        return (0, p + q) if p + q < 0.5 else (1, p + q - 1)
+    if lo >= 0:
+        return (2, -(p + q)) if p + q < 0.5 else (1, 1 - (p + q))
+    return (1, q - p)
 
 
 def route_ref(logits, k: int, *, score="softmax", bias=None, groups=1, top_groups=1, renormalize=True, scale=1.0):

@@ -7,8 +7,8 @@
 // chosen): without a bias, c orders as the logits themselves do, in both
 // scores, so the keys are the float32 logits and no score is computed for the
 // choice.  Where a group's score is the sum of two sigmoids, that sum is
-// formed in float64 from its two largest logits, and above one from what the
-// two lack of one: sigmoids of more than 36.7 are 1.0 in float64 already.
+// formed in float64 from its two largest logits, near one and two as its
+// distance from there: sigmoids of more than 36.7 are 1.0 in float64 already.
 // With a bias c itself is formed in float64, and scores that are equal there
 // are ties (sigmoids above 36.7 with one bias, scores below 2^-53 of a bias).
 // Each of the k
@@ -114,23 +114,23 @@ __device__ __forceinline__ uint64_t from_lane(uint64_t v, int l) {
 __device__ __forceinline__ Key64 pair_score(Key64 a, Key64 b) {
   return a.any() && b.any() ? Key64::of(a.value() + b.value()) : Key64::none();
 }
-// The same from two logits, c = sigmoid: s(a) + s(b), which exceeds one where
-// a + b > 0, and is then 2 - (s(-a) + s(-b)): the keys of what is missing, in
-// reverse, behind that of one.  (a >= b; exp of at most 0 but for one term.)
+// The same from two logits, a >= b and c = sigmoid.  With p = sigmoid(-|a|) and
+// q = sigmoid(-|b|), which hold their bits however small they are, the sum is
+// p + q, 1 + (q - p) or 2 - (p + q).  Its key goes by itself below 1/2, by what
+// it is from one up to 3/2, by what it lacks of two above.
 __device__ __forceinline__ Key64 pair_score(Key32 a, Key32 b) {
   if (!a.any() || !b.any()) return Key64::none();
-  double x = (double)a.value(), y = (double)b.value();
-  const bool over = x + y > 0.0;
-  if (over) {
-    x = -x;
-    y = -y;
+  const double x = (double)a.value(), y = (double)b.value();
+  const double ex = exp(-fabs(x)), ey = exp(-fabs(y));
+  const double p = ex / (1.0 + ex), q = ey / (1.0 + ey);
+  const uint64_t low = 0x3fe0ull << 48, middle = 0x7fc0ull << 48;  // keys of [0, 1/2], of [-1/2, 1/2]
+  const double s = p + q;
+  if (s < 0.5 && (x <= 0.0 || y >= 0.0)) {
+    const uint64_t at = (uint64_t)__double_as_longlong(s);
+    return {x <= 0.0 ? 1 + at : 4 + low + middle + (low - at)};
   }
-  const auto sigmoid = [](double v) {
-    const double e = exp(-fabs(v));
-    return (v > 0.0 ? 1.0 : e) / (1.0 + e);
-  };
-  const uint64_t s = Key64::of(sigmoid(x) + sigmoid(y)).v, one = Key64::of(1.0).v;
-  return {over ? one + (one - s) : s};
+  const double from_one = x <= 0.0 ? s - 1.0 : (y >= 0.0 ? 1.0 - s : q - p);
+  return {2 + low + (Key64::of(from_one).v - Key64::of(-0.5).v)};
 }
 
 // What the keys are: the logits; the logits, with groups by the sum of two

@@ -196,3 +196,25 @@ def test_scores_that_saturate(E, groups, top_groups, k):
         l = rng.uniform(lo, hi, size=(20, E))
         check(l, "f32", k, **kw)
         check(l, "bf16", k, renormalize=False, **kw)
+
+
+def test_group_sums_near_one():
+    """Groups of one large and one small logit, whose sums differ from one by
+    less than float64 holds beside it, of either sign; in between, sums of two
+    of a kind."""
+    rng = np.random.default_rng(9)
+    for n in (2, 3, 5):
+        l = np.full((60, 12 * n), -200.0)
+        for t in range(60):
+            for g in range(12):
+                a, b = rng.uniform(30, 90), rng.uniform(-90, -30)
+                l[t, g * n], l[t, g * n + n - 1] = (a, b) if t % 3 or g % 4 else rng.uniform(-1, 1, 2)
+        for top_groups in (1, 5, 11):
+            check(l, "f32", 2, score="sigmoid", groups=12, top_groups=top_groups)
+    # by hand: 1 - 2e-18 + 1e-17, 1 - 1e-17 + 2e-18, 1 exactly, 1 + 1e-20
+    l = np.log([[2e-18, 1e-17, 1e-17, 2e-18, 1e-19, 1e-19, 1e-20, 2e-20]])
+    l[0, ::2] *= -1
+    ids, _ = check(l, "f32", 2, score="sigmoid", groups=4, top_groups=1)
+    assert ids.tolist() == [[0, 1]]
+    ids, _ = check(l, "f32", 4, score="sigmoid", groups=4, top_groups=3)
+    assert 2 not in ids
