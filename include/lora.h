@@ -718,9 +718,9 @@ int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void
  * after every other in the sigmoid form (if it has two or more).
  * Without a bias the order of c is that of the logits, whatever a score
  * rounds to; a group's sum of two is compared in float64, near one and two as
- * its distance from there.  With a bias c is formed in float64,
- * and what is equal there is a tie: sigmoid scores of logits above 36.7 that
- * have one bias, scores below 2^-53 of theirs.
+ * its distance from there.  With a bias c is formed in float64, and what is
+ * equal there is a tie: sigmoid scores of logits above 36.7 that have one
+ * bias, scores below 2^-53 of theirs.
  *   logits [T, ldl] : dtype rows, ldl >= E, naturally aligned (no 16-byte
  *            rule).
  * Errors: INVALID_ARG (null pointers, T < 0, E < 1, k < 1, ldl < E, groups

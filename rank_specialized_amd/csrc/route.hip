@@ -11,10 +11,9 @@
 // distance from there: sigmoids of more than 36.7 are 1.0 in float64 already.
 // With a bias c itself is formed in float64, and scores that are equal there
 // are ties (sigmoids above 36.7 with one bias, scores below 2^-53 of a bias).
-// Each of the k
-// steps takes the wave's largest key (four lane exchanges and a scalar
-// maximum of the four rows) and its lowest index, and drops it; weights are
-// computed at the end, by the k lanes that hold the chosen logits.
+// Each of the k steps takes the wave's largest key (four lane exchanges and a
+// scalar maximum of the four rows) and its lowest index, and drops it; weights
+// are computed at the end, by the k lanes that hold the chosen logits.
 //
 // What bounds it is the length of a wave's chain, not the bytes: one token of
 // 64 experts 2.7 us (the shortest fill kernel: 1.3), 8192 tokens of 128 (4.7

@@ -20,9 +20,9 @@
 // Measured (kernel times, three sets of weights in turn): one token 3584 ->
 // 18944 9.3 to 9.7 us (35.6 MB, 3.7 TB/s); 23 rows 18944 -> 3584 in groups of
 // 64 14.6 (2.6) and 3.9 for the splits' sum; one token's eight experts of 64,
-// 2048 -> 2816, 8.1 (23.8 MB, 2.9), eight tokens' 28.7 (about 120 MB, 4.2); 180 rows
-// of 32 experts 1408 -> 2048 in groups of 32 18.2 (2.9): with few bytes the
-// launch, the copy of x and the last sums show, with fine groups the
+// 2048 -> 2816, 8.1 (23.8 MB, 2.9), eight tokens' 28.7 (about 120 MB, 4.2);
+// 180 rows of 32 experts 1408 -> 2048 in groups of 32 18.2 (2.9): with few
+// bytes the launch, the copy of x and the last sums show, with fine groups the
 // instructions per code.  The codes' loads go through the caches (past them,
 // as data read once, one token took 10.4, the 23 rows 16.2).  More waves in a
 // workgroup rather than more tiles in a wave's flight: one token 9.3 us with
