@@ -697,6 +697,104 @@ int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void
                           size_t ws_bytes, void* stream);
 
 /*
+ * 8-bit base layers: weights and activations as 8-bit integers, products on
+ * the integer matrix cores.  A w8 store holds one matrix with a scale per
+ * output (a channel), and a row of activations has a scale of its own (a
+ * token):
+ *
+ *     y[t, o] = s_x[t] s_w[o] sum_k q_x[t, k] q_w[o, k]
+ *
+ * The sum is an exact 32-bit integer; it is taken to float32, multiplied with
+ * s_x[t], then with s_w[o], and y rounds once.
+ *   codes, scales : the caller's buffers, laid out by lora_w8_pack.
+ * A plain struct; the caller owns the buffers and keeps them alive.
+ */
+typedef struct lora_w8_store {
+  int32_t d_in;
+  int32_t d_out;
+  const void* codes;
+  const void* scales;
+} lora_w8_store;
+
+/* Largest d_in (128 * 128 * d_in stays below 2^31) and d_out, most rows of a
+ * call, largest row stride of codes. */
+#define LORA_W8_MAX_IN 131064
+#define LORA_W8_MAX_OUT (1 << 20)
+#define LORA_W8_MAX_ROWS (1 << 20)
+#define LORA_W8_MAX_LDQ (1 << 22)
+
+/*
+ * Size query (host only): bytes of a w8 store's two buffers.  Errors:
+ * INVALID_ARG (null outputs, d < 1); UNSUPPORTED (d not a multiple of 8, d_in
+ * above LORA_W8_MAX_IN, d_out above LORA_W8_MAX_OUT).
+ */
+int lora_w8_bytes(int d_in, int d_out, size_t* code_bytes_host, size_t* scale_bytes_host);
+
+/*
+ * Lay a checkpoint's matrix out.
+ *   q      [d_out][d_in] : codes -128..127, 8-byte aligned.
+ *   scales [d_out]       : scale_dtype; held as float32.
+ *   codes, out_scales    : lora_w8_bytes' sizes, 16-byte aligned.
+ *   out_host             : filled on success; the inputs are not referenced.
+ * Errors: as lora_w8_bytes; INVALID_ARG for null pointers; UNSUPPORTED for
+ * misaligned ones and an unknown scale dtype.
+ */
+int lora_w8_pack(lora_w8_store* out_host, int d_in, int d_out, const int8_t* q, const void* scales, int scale_dtype,
+                 void* codes, float* out_scales, void* stream);
+
+/*
+ * Rows rounded to 8-bit integers with a scale each (a row may be a token's
+ * activations, or an output's weights):
+ *
+ *     scales[t] = a / 127,  q[t, k] = 127 x[t, k] / a,  a = max_k |x[t, k]|,
+ *
+ * q the nearest integer to the exact quotient, the even one of two as near.
+ * A row of zeros has scale 0 and codes 0; a row with an infinity or a NaN the
+ * scale NaN and codes 0.
+ *   x [T, ldx] : dtype rows as in the conventions above, d_in a multiple of 8.
+ *   q [T, ldq] : out; ldq a multiple of 16, q 16-byte aligned.  Bytes past
+ *                d_in are not written.
+ *   scales [T] : out, float32.
+ * Enqueues one kernel.  Errors: INVALID_ARG (null pointers, T < 0, d_in < 1,
+ * ldx or ldq < d_in); UNSUPPORTED (d_in as lora_w8_bytes, alignment, T above
+ * LORA_W8_MAX_ROWS, ldq above LORA_W8_MAX_LDQ, unknown dtype).
+ */
+int lora_w8_quantize(int dtype, const void* x, int64_t ldx, int T, int d_in, int8_t* q, int64_t ldq, float* scales,
+                     void* stream);
+
+/*
+ * Workspace of lora_w8_apply (quantized = 0) or lora_w8_apply_quantized for T
+ * rows (host only; 0 when none is needed, and on invalid arguments).  Scratch:
+ * no initialization, and not shared by calls in flight together.
+ */
+size_t lora_w8_workspace_bytes(const lora_w8_store* store_host, int T, int quantized);
+
+/*
+ * The 8-bit base layer, from one decode token to a prefill step.  y is
+ * overwritten (add the adapters' branch to it with lora_apply_batched or
+ * lora_apply_planned).
+ *   lora_w8_apply           : rows of x, rounded as lora_w8_quantize does.
+ *   lora_w8_apply_quantized : rows that lora_w8_quantize (or a caller) has
+ *                             rounded, for several layers of one input.
+ *   dtype : of y (and x).
+ *   q [T, ldq] : codes -128..127; ldq a multiple of 16, 16-byte aligned.  Rows
+ *                are read in pieces of 16 bytes, the last row's last one too;
+ *                the bytes past d_in may hold anything.
+ * The two give the same y, bit for bit, on the same codes and scales, and from
+ * call to call.  A row of x with an infinity or a NaN gives a row of y without
+ * finite values; other rows are not touched by it.  A sum times s_x[t] that
+ * float32 does not hold gives an infinity whatever s_w[o] is.
+ * Enqueues one or two kernels.
+ * Errors: INVALID_ARG (null pointers, T < 0, ldx or ldq < d_in, ldy < d_out, ws
+ * too small); UNSUPPORTED (sizes as lora_w8_bytes, alignment, T above
+ * LORA_W8_MAX_ROWS, ldq above LORA_W8_MAX_LDQ, unknown dtype).
+ */
+int lora_w8_apply(const lora_w8_store* store_host, int dtype, const void* x, int64_t ldx, void* y, int64_t ldy, int T,
+                  void* ws, size_t ws_bytes, void* stream);
+int lora_w8_apply_quantized(const lora_w8_store* store_host, const int8_t* q, int64_t ldq, const float* scales, int dtype,
+                            void* y, int64_t ldy, int T, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * The router: each token's k experts of E, from its logits l[t, :].
  *   score  : s = softmax(l[t]) over the E experts (LORA_ROUTE_SOFTMAX) or
  *            s_e = 1 / (1 + exp(-l_e)) (LORA_ROUTE_SIGMOID).

@@ -38,7 +38,8 @@ __all__ = [
     "lora_jd_apply", "lora_ranks_uniform", "lora_ranks_spectral", "RsvdFactors", "lora_rsvd_workspace_bytes",
     "lora_rsvd_factor", "lora_rsvd_write", "MultiStore", "lora_pack_multi", "lora_multi_workspace_bytes",
     "lora_apply_multi", "W4Store", "lora_w4_bytes", "lora_w4_pack", "lora_w4_workspace_bytes", "lora_w4_apply",
-    "lora_w4_apply_experts", "lora_route", "load_library",
+    "lora_w4_apply_experts", "lora_route", "W8Store", "lora_w8_bytes", "lora_w8_pack", "lora_w8_quantize",
+    "lora_w8_workspace_bytes", "lora_w8_apply", "lora_w8_apply_quantized", "load_library",
 ]
 
 _DTYPES = {torch.bfloat16: L.LORA_DTYPE_BF16, torch.float32: L.LORA_DTYPE_F32}
@@ -854,3 +855,170 @@ def lora_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Op
     _call("lora_route", index, _p(logits), ldl, dt, T, E, k, mode, bias.data_ptr() if bias is not None else None,
           _int(groups, "groups"), _int(top_groups, "top_groups"), int(renormalize), float(scale), _p(ids), _p(weights))
     return ids, weights
+
+
+@dataclass
+class W8Store:
+    """An 8-bit matrix laid out by lora_w8_pack: the C struct plus its buffers."""
+
+    c: L.lora_w8_store
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def __post_init__(self):
+        c = self.c
+        self.d_in, self.d_out = c.d_in, c.d_out
+        self.device_index = self.codes.get_device()
+        if self.device_index < 0 or self.scales.get_device() != self.device_index:
+            raise ValueError("codes and scales must be on one GPU")
+        self._ref = C.byref(c)
+        self._ws_bytes = {}
+
+    def ref(self):
+        return self._ref
+
+    def clone(self) -> "W8Store":
+        """An independent copy in fresh device memory (same layout)."""
+        codes, scales = self.codes.clone(), self.scales.clone()
+        c = L.lora_w8_store.from_buffer_copy(self.c)
+        c.codes, c.scales = codes.data_ptr(), scales.data_ptr()
+        return W8Store(c, codes, scales)
+
+
+def lora_w8_bytes(d_in: int, d_out: int):
+    """Bytes of a w8 store's codes and scales buffers."""
+    a, b = C.c_size_t(), C.c_size_t()
+    L.check("lora_w8_bytes", L.lib().lora_w8_bytes(_int(d_in, "d_in"), _int(d_out, "d_out"), C.byref(a), C.byref(b)))
+    return a.value, b.value
+
+
+def lora_w8_pack(q: torch.Tensor, scales: torch.Tensor) -> W8Store:
+    """Lay an 8-bit matrix out: W[o, k] = scales[o] * q[o, k].
+
+    q: int8 [d_out, d_in]; scales (bfloat16 or float32) [d_out]."""
+    if q.dim() != 2 or q.dtype != torch.int8:
+        raise ValueError("q must be int8 [d_out, d_in]")
+    d_out, d_in = q.shape
+    if scales.shape != (d_out,):
+        raise ValueError(f"scales must be [{d_out}]")
+    sd = _dtype(scales, "scales")
+    index = q.get_device()
+    _same_device(index, scales=scales)
+    q, scales = q.contiguous(), scales.contiguous()
+    cb, sb = lora_w8_bytes(d_in, d_out)
+    codes = torch.empty(cb, dtype=torch.uint8, device=q.device)
+    out = torch.empty(sb // 4, dtype=torch.float32, device=q.device)
+    c = L.lora_w8_store()
+    _call("lora_w8_pack", index, C.byref(c), d_in, d_out, _p(q), _p(scales), sd, codes.data_ptr(), out.data_ptr())
+    return W8Store(c, codes, out)
+
+
+def _codes(q: torch.Tensor, T: int, d_in: int, name: str) -> int:
+    """Row stride of int8 [T, d_in] rows, whose memory has to reach to a
+    multiple of 16 values behind the last."""
+    if q.dtype != torch.int8 or q.shape != (T, d_in):
+        raise ValueError(f"{name} must be int8 [{T}, {d_in}]")
+    ld = _ld(q, name) if T > 1 else (d_in + 15) // 16 * 16
+    if T > 0 and d_in > 1 and q.stride(1) != 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    if T > 0 and d_in % 16 != 0:
+        end = q.storage_offset() + (T - 1) * ld + (d_in + 15) // 16 * 16
+        if end > q.untyped_storage().nbytes():
+            raise ValueError(f"{name}'s last row must reach to a multiple of 16 values in memory")
+    return ld
+
+
+def lora_w8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None):
+    """Rows rounded to 8-bit integers: (q int8 [T, d_in], scales float32 [T]),
+    x[t, k] ~ scales[t] q[t, k], scales[t] = max |x[t]| / 127.
+
+    q's rows start at multiples of 16 values (its row stride is d_in rounded up
+    to one, unless q is given)."""
+    dt, ldx, index = _dtype(x, "x"), _ld(x, "x"), x.get_device()
+    T, d_in = x.shape
+    if index < 0:
+        _same_device(index)
+    if q is None:
+        q = torch.empty(T, (d_in + 15) // 16 * 16, dtype=torch.int8, device=x.device)[:, :d_in]
+    else:
+        _same_device(index, q=q)
+    ldq = _codes(q, T, d_in, "q")
+    if scales is None:
+        scales = torch.empty(T, dtype=torch.float32, device=x.device)
+    elif scales.shape != (T,) or scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError("scales must be a contiguous float32 [T]")
+    else:
+        _same_device(index, scales=scales)
+    _call("lora_w8_quantize", index, dt, _p(x), ldx, T, d_in, _p(q), ldq, _p(scales))
+    return q, scales
+
+
+def lora_w8_workspace_bytes(store: W8Store, T: int, quantized: bool = False) -> int:
+    """Workspace of lora_w8_apply, or of lora_w8_apply_quantized, for T rows."""
+    return int(L.lib().lora_w8_workspace_bytes(store.ref(), _int(T, "T"), int(quantized)))
+
+
+def _w8_out(store: W8Store, T: int, y, dtype: torch.dtype, device):
+    """y, and its row stride."""
+    if y is None:
+        return torch.empty(T, store.d_out, dtype=dtype, device=device), store.d_out
+    if y.shape != (T, store.d_out) or y.dtype != dtype:
+        raise ValueError(f"y must be [{T}, {store.d_out}] of {dtype}")
+    _same_device(store.device_index, y=y)
+    return y, _ld(y, "y")
+
+
+def _w8_ws(store: W8Store, T: int, quantized: bool, ws, device):
+    """(the workspace tensor, to be held until the call; its pointer; its bytes)"""
+    if ws is not None:
+        _same_device(store.device_index, ws=ws)
+        return ws, _p(ws), _scratch(ws)
+    key = (T, quantized)
+    nb = store._ws_bytes.get(key)
+    if nb is None:
+        if len(store._ws_bytes) >= 1024:
+            store._ws_bytes.clear()
+        nb = store._ws_bytes[key] = lora_w8_workspace_bytes(store, T, quantized)
+    if nb == 0:
+        return None, None, 0
+    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), nb
+
+
+def lora_w8_apply(store: W8Store, x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                  ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[t] = W x[t] (overwrites y; allocated when None): the 8-bit base layer,
+    x [T, d_in] bfloat16 or float32, rounded to 8-bit integers on the way."""
+    dt, ldx, index = _dtype(x, "x"), _ld(x, "x"), store.device_index
+    T = x.shape[0]
+    if x.shape[1] != store.d_in:
+        raise ValueError("x must have d_in columns")
+    if x.get_device() != index:
+        _same_device(index, x=x)
+    y, ldy = _w8_out(store, T, y, x.dtype, x.device)
+    ws, ws_ptr, nb = _w8_ws(store, T, False, ws, x.device)
+    _call("lora_w8_apply", index, store._ref, dt, _p(x), ldx, _p(y), ldy, T, ws_ptr, nb)
+    return y
+
+
+def lora_w8_apply_quantized(store: W8Store, q: torch.Tensor, scales: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                            dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The 8-bit base layer of rows that lora_w8_quantize has rounded (several
+    layers of one input share them): y [T, d_out] of `dtype`, or of y's own."""
+    index = store.device_index
+    if q.dim() != 2:
+        raise ValueError("q must be int8 [T, d_in]")
+    T = q.shape[0]
+    ldq = _codes(q, T, store.d_in, "q")
+    if scales.shape != (T,) or scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError("scales must be a contiguous float32 [T]")
+    _same_device(index, q=q, scales=scales)
+    if y is not None:
+        dtype = y.dtype
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError("y must be bfloat16 or float32")
+    y, ldy = _w8_out(store, T, y, dtype, q.device)
+    ws, ws_ptr, nb = _w8_ws(store, T, True, ws, q.device)
+    _call("lora_w8_apply_quantized", index, store._ref, _p(q), ldq, _p(scales), dt, _p(y), ldy, T, ws_ptr, nb)
+    return y

@@ -56,9 +56,17 @@ class lora_w4_store(C.Structure):
     ]
 
 
+class lora_w8_store(C.Structure):
+    _fields_ = [("d_in", C.c_int32), ("d_out", C.c_int32), ("codes", C.c_void_p), ("scales", C.c_void_p)]
+
+
 LORA_W4_MAX_N = 1024
 LORA_W4_MAX_DIM = 1 << 20
 LORA_W4_MAX_ROWS = 1 << 20
+LORA_W8_MAX_IN = 131064
+LORA_W8_MAX_OUT = 1 << 20
+LORA_W8_MAX_ROWS = 1 << 20
+LORA_W8_MAX_LDQ = 1 << 22
 LORA_ROUTE_SOFTMAX = 0
 LORA_ROUTE_SIGMOID = 1
 LORA_ROUTE_MAX_EXPERTS = 1024
@@ -108,6 +116,12 @@ SIGNATURES = {
     "lora_w4_workspace_bytes": (SZ, [C.POINTER(lora_w4_store), I, I, I, I]),
     "lora_w4_apply": (I, [C.POINTER(lora_w4_store), I, P, I64, P, I64, I, P, SZ, P]),
     "lora_w4_apply_experts": (I, [C.POINTER(lora_w4_store), I, P, I64, I, P, I64, I, I, P, P, P, SZ, P]),
+    "lora_w8_bytes": (I, [I, I, C.POINTER(SZ), C.POINTER(SZ)]),
+    "lora_w8_pack": (I, [C.POINTER(lora_w8_store), I, I, P, P, I, P, P, P]),
+    "lora_w8_quantize": (I, [I, P, I64, I, I, P, I64, P, P]),
+    "lora_w8_workspace_bytes": (SZ, [C.POINTER(lora_w8_store), I, I]),
+    "lora_w8_apply": (I, [C.POINTER(lora_w8_store), I, P, I64, P, I64, I, P, SZ, P]),
+    "lora_w8_apply_quantized": (I, [C.POINTER(lora_w8_store), P, I64, P, I, P, I64, I, P, SZ, P]),
     "lora_route": (I, [P, I64, I, I, I, I, I, P, I, I, I, C.c_float, P, P, P]),
 }
 
