@@ -697,6 +697,48 @@ int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void
                           size_t ws_bytes, void* stream);
 
 /*
+ * A whole mixture-of-experts layer for a few tokens (a decode step), in two
+ * kernels: each of T tokens takes k experts, ids [T, k], with weights [T, k]
+ * (both as lora_route writes them), and expert e is three matrices,
+ *
+ *     y[t] = sum_j weights[t, j] D_e (act(G_e x[t]) * (U_e x[t])),   e = ids[t, j]
+ *
+ * held as gate and up [ffn, d_in] and down [d_out, ffn]: three w4 stores of
+ * the same number of experts, gate and up alike in group, scale dtype and zero
+ * points (down may differ in those).
+ *   act : LORA_MOE_SILU, g / (1 + exp(-g)), or LORA_MOE_GELU_TANH,
+ *         g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))).
+ *   x [T, ldx], y [T, ldy] : dtype rows as in the conventions above.  y is
+ *         overwritten.
+ * An id outside [0, n) names no expert and adds nothing, whatever its weight
+ * (a token without any gets a row of zeros); the same id may appear twice in a
+ * token: it counts with the sum of its weights.  A weight that is infinite or
+ * NaN, or a row of x with such a value, gives a row of y without finite values
+ * (where an expert is named); other rows are not touched by it.
+ * Sums are float32 in a fixed order, results do not change from call to call.
+ * act(g) * u is held to 16 bits for bf16 rows, in whole for float32 ones; y
+ * rounds once.  Codes are multiplied as in lora_w4_apply's few rows.
+ * For more tokens there is lora_w4_apply_experts.
+ * Errors: INVALID_ARG (null pointers, T < 0, k < 1, ldx < d_in, ldy < d_out,
+ * stores that do not fit together, an unknown act, ws too small); UNSUPPORTED
+ * (sizes as lora_w4_bytes, ffn above LORA_W4_MOE_MAX_FFN, T above
+ * LORA_W4_MOE_MAX_TOKENS, k above LORA_W4_MOE_MAX_K, unknown dtype, alignment).
+ *
+ * lora_w4_moe_workspace_bytes: bytes of ws (host only; 0 when T is 0, and on
+ * invalid arguments).  Scratch: no initialization, and not shared by calls in
+ * flight together.
+ */
+enum lora_moe_act { LORA_MOE_SILU = 0, LORA_MOE_GELU_TANH = 1 };
+#define LORA_W4_MOE_MAX_TOKENS 64
+#define LORA_W4_MOE_MAX_K 32
+#define LORA_W4_MOE_MAX_FFN 16384
+size_t lora_w4_moe_workspace_bytes(const lora_w4_store* gate_host, const lora_w4_store* up_host,
+                                   const lora_w4_store* down_host, int dtype, int T, int k);
+int lora_w4_moe(const lora_w4_store* gate_host, const lora_w4_store* up_host, const lora_w4_store* down_host, int dtype,
+                int act, const void* x, int64_t ldx, void* y, int64_t ldy, int T, int k, const int32_t* ids,
+                const float* weights, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * 8-bit base layers: weights and activations as 8-bit integers, products on
  * the integer matrix cores.  A w8 store holds one matrix with a scale per
  * output (a channel), and a row of activations has a scale of its own (a

@@ -38,7 +38,7 @@ __all__ = [
     "lora_jd_apply", "lora_ranks_uniform", "lora_ranks_spectral", "RsvdFactors", "lora_rsvd_workspace_bytes",
     "lora_rsvd_factor", "lora_rsvd_write", "MultiStore", "lora_pack_multi", "lora_multi_workspace_bytes",
     "lora_apply_multi", "W4Store", "lora_w4_bytes", "lora_w4_pack", "lora_w4_workspace_bytes", "lora_w4_apply",
-    "lora_w4_apply_experts", "lora_route", "W8Store", "lora_w8_bytes", "lora_w8_pack", "lora_w8_quantize",
+    "lora_w4_apply_experts", "lora_route", "lora_w4_moe_workspace_bytes", "lora_w4_moe", "W8Store", "lora_w8_bytes", "lora_w8_pack", "lora_w8_quantize",
     "lora_w8_workspace_bytes", "lora_w8_apply", "lora_w8_apply_quantized", "load_library",
 ]
 
@@ -855,6 +855,60 @@ def lora_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: Op
     _call("lora_route", index, _p(logits), ldl, dt, T, E, k, mode, bias.data_ptr() if bias is not None else None,
           _int(groups, "groups"), _int(top_groups, "top_groups"), int(renormalize), float(scale), _p(ids), _p(weights))
     return ids, weights
+
+
+_ACTS = {"silu": L.LORA_MOE_SILU, "gelu_tanh": L.LORA_MOE_GELU_TANH}
+
+
+def lora_w4_moe_workspace_bytes(gate: W4Store, up: W4Store, down: W4Store, dtype: torch.dtype, T: int, k: int) -> int:
+    """Workspace of lora_w4_moe for T tokens of k experts each."""
+    return int(L.lib().lora_w4_moe_workspace_bytes(gate.ref(), up.ref(), down.ref(), _DTYPES[dtype], _int(T, "T"), _int(k, "k")))
+
+
+def lora_w4_moe(gate: W4Store, up: W4Store, down: W4Store, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                y: Optional[torch.Tensor] = None, *, act: str = "silu", ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A mixture-of-experts layer for a few tokens (at most 64):
+    y[t] = sum_j weights[t, j] D_e (act(G_e x[t]) * (U_e x[t])), e = ids[t, j].
+
+    gate and up: stores of n experts [ffn, d_in], down: of [d_out, ffn];
+    x [T, d_in] bfloat16 or float32; ids (int32) and weights (float32) [T, k]
+    as lora_route gives them (an id outside [0, n) names no expert); act
+    "silu" or "gelu_tanh".  Overwrites y [T, d_out]; allocated when None."""
+    dt, ldx, index = _dtype(x, "x"), _ld(x, "x"), gate.device_index
+    if ids.dim() != 2 or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 [T, k]")
+    T, k = ids.shape
+    if k > _INT_MAX:
+        raise ValueError("ids has more columns than an int counts")
+    if x.shape != (T, gate.d_in):
+        raise ValueError("x must be [T, d_in]")
+    if weights.shape != ids.shape or weights.dtype != torch.float32 or not weights.is_contiguous():
+        raise ValueError("weights must be a contiguous float32 [T, k]")
+    mode = _ACTS.get(act)
+    if mode is None:
+        raise ValueError("act must be 'silu' or 'gelu_tanh'")
+    if up.device_index != index or down.device_index != index:
+        raise ValueError("gate, up and down must be on one GPU")
+    _same_device(index, x=x, ids=ids, weights=weights)
+    if y is None:
+        ldy = down.d_out
+        y = torch.empty(T, ldy, dtype=x.dtype, device=x.device)
+    else:
+        if y.shape != (T, down.d_out) or y.dtype != x.dtype:
+            raise ValueError(f"y must be [{T}, {down.d_out}] of x's dtype")
+        _same_device(index, y=y)
+        ldy = _ld(y, "y")
+    if ws is None:
+        nb = lora_w4_moe_workspace_bytes(gate, up, down, x.dtype, T, k)
+        if nb:
+            ws = torch.empty(nb, dtype=torch.uint8, device=x.device)
+        ws_ptr = ws.data_ptr() if nb else None
+    else:
+        _same_device(index, ws=ws)
+        nb, ws_ptr = _scratch(ws), _p(ws)
+    _call("lora_w4_moe", index, gate._ref, up._ref, down._ref, dt, mode, _p(x), ldx, _p(y), ldy, T, k, _p(ids),
+          _p(weights), ws_ptr, nb)
+    return y
 
 
 @dataclass

@@ -63,6 +63,11 @@ class lora_w8_store(C.Structure):
 LORA_W4_MAX_N = 1024
 LORA_W4_MAX_DIM = 1 << 20
 LORA_W4_MAX_ROWS = 1 << 20
+LORA_MOE_SILU = 0
+LORA_MOE_GELU_TANH = 1
+LORA_W4_MOE_MAX_TOKENS = 64
+LORA_W4_MOE_MAX_K = 32
+LORA_W4_MOE_MAX_FFN = 16384
 LORA_W8_MAX_IN = 131064
 LORA_W8_MAX_OUT = 1 << 20
 LORA_W8_MAX_ROWS = 1 << 20
@@ -116,6 +121,9 @@ SIGNATURES = {
     "lora_w4_workspace_bytes": (SZ, [C.POINTER(lora_w4_store), I, I, I, I]),
     "lora_w4_apply": (I, [C.POINTER(lora_w4_store), I, P, I64, P, I64, I, P, SZ, P]),
     "lora_w4_apply_experts": (I, [C.POINTER(lora_w4_store), I, P, I64, I, P, I64, I, I, P, P, P, SZ, P]),
+    "lora_w4_moe_workspace_bytes": (SZ, [C.POINTER(lora_w4_store), C.POINTER(lora_w4_store), C.POINTER(lora_w4_store), I, I, I]),
+    "lora_w4_moe": (I, [C.POINTER(lora_w4_store), C.POINTER(lora_w4_store), C.POINTER(lora_w4_store), I, I, P, I64, P, I64,
+                        I, I, P, P, P, SZ, P]),
     "lora_w8_bytes": (I, [I, I, C.POINTER(SZ), C.POINTER(SZ)]),
     "lora_w8_pack": (I, [C.POINTER(lora_w8_store), I, I, P, P, I, P, P, P]),
     "lora_w8_quantize": (I, [I, P, I64, I, I, P, I64, P, P]),
