@@ -19,25 +19,38 @@ struct MoeEntry {
 // does not see it), of float32 rows both are whole.
 constexpr int moe_h_parts(int dtype) { return dtype == LORA_DTYPE_BF16 ? 2 : 3; }
 
+// 16-output blocks of d_out that a workgroup of the second kernel owns.
+constexpr int kMoeDownBlocks = 8;
+inline int moe_down_groups(int d_out) { return (w4_row_tiles(d_out) + kMoeDownBlocks - 1) / kMoeDownBlocks; }
+
 struct MoePlan {
   int entries;       // rows of the table: the choices, or the experts
   bool by_row;
   int h_tiles;       // tiles of 128 of a row of h
   size_t h, table;   // h [T k][parts][h_tiles * 128] bf16
+  size_t part;       // [T k][d_out] float32: the choices' weighted outputs
+  size_t counted;    // [T k] bytes: whether a choice has such a row
+  size_t arrived;    // [moe_down_groups] workgroups that have written theirs
   size_t ws_bytes;
 };
 
-inline MoePlan moe_plan_call(int n, int ffn, int dtype, int T, int k) {
+inline MoePlan moe_plan_call(int n, int ffn, int d_out, int dtype, int T, int k) {
   MoePlan p{};
   if (T <= 0) return p;
   const int R = T * k;
   p.by_row = R <= n;
   p.entries = p.by_row ? R : n;
   p.h_tiles = w4_k_tiles(ffn);
-  p.h = 0;
-  p.ws_bytes = align_up((size_t)R * (size_t)moe_h_parts(dtype) * (size_t)p.h_tiles * kW4K * 2, 256);
-  p.table = p.ws_bytes;
-  p.ws_bytes += align_up((size_t)p.entries * sizeof(MoeEntry), 256);
+  auto take = [&](size_t bytes) {
+    const size_t at = p.ws_bytes;
+    p.ws_bytes += align_up(bytes, 256);
+    return at;
+  };
+  p.h = take((size_t)R * (size_t)moe_h_parts(dtype) * (size_t)p.h_tiles * kW4K * 2);
+  p.table = take((size_t)p.entries * sizeof(MoeEntry));
+  p.part = take((size_t)R * (size_t)d_out * 4);
+  p.counted = take((size_t)R);
+  p.arrived = take((size_t)moe_down_groups(d_out) * 4);
   return p;
 }
 

@@ -34,7 +34,7 @@ extern "C" {
 size_t lora_w4_moe_workspace_bytes(const lora_w4_store* gate_host, const lora_w4_store* up_host,
                                    const lora_w4_store* down_host, int dtype, int T, int k) {
   if (check_moe_stores(gate_host, up_host, down_host) != LORA_OK || check_moe_sizes(dtype, T, k) != LORA_OK) return 0;
-  return moe_plan_call(gate_host->n, gate_host->d_out, dtype, T, k).ws_bytes;
+  return moe_plan_call(gate_host->n, gate_host->d_out, down_host->d_out, dtype, T, k).ws_bytes;
 }
 
 int lora_w4_moe(const lora_w4_store* gate_host, const lora_w4_store* up_host, const lora_w4_store* down_host, int dtype,
@@ -62,7 +62,7 @@ int lora_w4_moe(const lora_w4_store* gate_host, const lora_w4_store* up_host, co
   c.k = k;
   c.ids = ids;
   c.weights = weights;
-  c.plan = moe_plan_call(c.gate.n, c.gate.d_out, dtype, T, k);
+  c.plan = moe_plan_call(c.gate.n, c.gate.d_out, c.down.d_out, dtype, T, k);
   if ((st = check_w4_ws(ws, ws_bytes, c.plan.ws_bytes)) != LORA_OK) return st;
   if (T == 0) return LORA_OK;
   c.ws = reinterpret_cast<char*>(ws);

@@ -4,19 +4,22 @@
 //   y[t]    = sum_j w[t, j] D_e h[t, e]
 //
 // with 4-bit matrices (w4.h).  What bounds both is the stream of codes.  In
-// both, codes enter the bf16 matrix cores as in the few-rows products
-// (w4_rows.h): 32 + q with (32 + z) times the rows' sum taken off, or, for
-// float32 rows, q - z itself.
+// both, a workgroup owns 16 WB outputs of one expert for the tokens that chose
+// it: the rows lie in LDS, WK waves share the 128-input tiles of 16 outputs,
+// and their sums meet in LDS, in wave order.  Codes enter the bf16 matrix cores
+// as in the few-rows products (w4_rows.h): 32 + q with (32 + z) times the rows'
+// sum taken off, or, for float32 rows, q - z itself.
 //
-// Kernel 1: a workgroup owns 16 WB features of one expert, gate and up, for
-// the tokens that chose it (found by every wave alone, a token per lane); WK
-// waves share the inputs of 16 features, and their sums meet in LDS.  h leaves
-// as bf16 parts, the operands of the second kernel, and the expert's tokens as
-// an entry of a table.
-// Kernel 2: a workgroup owns 16 WB outputs of all tokens and walks the table;
-// WE waves share the tiles of 16 outputs.  Each wave adds its weighted sums to
-// rows of its own in LDS, which are added in wave order at the end: sums have
-// one order, whatever the schedule.
+// Rows that are more than one bf16 number wide are several rows of a product:
+// of bf16 tokens x is one and h two, of float32 tokens three each.  For a few
+// tokens they share one 16 x 16 product that would be mostly empty otherwise.
+//
+// Kernel 1 (gate and up): every wave finds the expert's tokens by itself, a
+// token per lane.  h leaves as bf16 parts, the rows of the second kernel, and
+// the tokens as an entry of a table.
+// Kernel 2 (down): a workgroup leaves weighted float32 rows, and the one that
+// comes last of those that share its outputs adds each token's, in order of its
+// choices: sums have one order, whatever the schedule.
 #pragma once
 #include "host_util.h"
 #include "moe_kernels.h"
@@ -25,44 +28,139 @@
 namespace lora {
 namespace {
 
-constexpr int kMoePad = 17;  // LDS row stride of a 16 x 16 block of sums
-constexpr int kMoeRows = 16;
+constexpr int kMoePad = 17;          // LDS row stride of a 16 x 16 block of sums
+constexpr int kMoeLds = 76 * 1024;   // of rows: two workgroups to a compute unit
 
-// The products of one tile of 128 inputs: rows at `x` (this lane's row and
-// piece) in PARTS planes, codes and scales of NB blocks of 16 outputs.
-template <int PARTS, bool EXACT, int SUB, int NB, typename Par>
-__device__ __forceinline__ void moe_tile(const char* x, int plane, const uint4 (&code)[NB], const Par (&par)[NB],
-                                         uint32_t mask, uint32_t magic, f32x4_t (&acc)[NB]) {
-  constexpr int kSteps = 4 / SUB;
-  const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-#pragma unroll
-  for (int s = 0; s < SUB; ++s) {
-    uint4 xp[kSteps][PARTS];
-    f32x4_t xsum = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < kSteps; ++j)
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        xp[j][q] = ld16(x + q * plane + 64 * (s * kSteps + j));
-        if constexpr (!EXACT) xsum = mfma_bf16_16x16x32(xp[j][q], ones, xsum);
-      }
+// The tiles of codes of NB blocks of 16 outputs, U of each in flight, and their
+// products with 16 NT rows.
+template <int KIND, int SUB, bool EXACT, int NB, int NT, int WK, int U>
+struct MoeStream {
+  typedef W4Params<KIND, SUB> Par;
+  const char *code0[NB], *par0[NB];  // uniform
+  uint32_t lane_code, lane_par;
+  uint4 code[U][NB];
+  Par par[U][NB];
+  uint32_t mask, magic;
+
+  __device__ __forceinline__ void fetch(int u, int kt) {
 #pragma unroll
     for (int a = 0; a < NB; ++a) {
-      const uint32_t cw[4] = {code[a].x, code[a].y, code[a].z, code[a].w};
-      const float sc = par[a].scale(s), z32 = par[a].zero32(s);
-      f32x4_t c;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) c[v] = EXACT ? 0.f : -z32 * xsum[v];
-#pragma unroll
-      for (int j = 0; j < kSteps; ++j) {
-        const uint4 b = EXACT ? w4_expand_exact(cw[s * kSteps + j], mask, magic, z32) : w4_expand(cw[s * kSteps + j], mask, magic);
-#pragma unroll
-        for (int q = 0; q < PARTS; ++q) c = mfma_bf16_16x16x32(xp[j][q], b, c);
-      }
-#pragma unroll
-      for (int v = 0; v < 4; ++v) acc[a][v] = fmaf(sc, c[v], acc[a][v]);
+      code[u][a] = ld16(code0[a] + (int64_t)kt * kW4TileBytes + lane_code);
+      par[u][a].load(par0[a] + (int64_t)kt * (kW4Rows * Par::kBytes) + lane_par);
     }
   }
+  __device__ __forceinline__ void start(int wk, int c0, int c1) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) fetch(u, min(c0 + wk + u * WK, c1 - 1));
+  }
+  // The products of one tile: x at this lane's row and piece.
+  __device__ __forceinline__ void tile(int u, const char* const (&x)[NT], uint32_t at, f32x4_t (&acc)[NB][NT]) {
+    constexpr int kSteps = 4 / SUB;
+    const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+#pragma unroll
+    for (int s = 0; s < SUB; ++s) {
+      uint4 b[NB][kSteps];
+#pragma unroll
+      for (int a = 0; a < NB; ++a) {
+        const uint32_t cw[4] = {code[u][a].x, code[u][a].y, code[u][a].z, code[u][a].w};
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j)
+          b[a][j] = EXACT ? w4_expand_exact(cw[s * kSteps + j], mask, magic, par[u][a].zero32(s))
+                          : w4_expand(cw[s * kSteps + j], mask, magic);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint4 xp[kSteps];
+        f32x4_t xsum = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kSteps; ++j) {
+          xp[j] = ld16(x[t] + at + 64 * (s * kSteps + j));
+          if constexpr (!EXACT) xsum = mfma_bf16_16x16x32(xp[j], ones, xsum);
+        }
+#pragma unroll
+        for (int a = 0; a < NB; ++a) {
+          const float sc = par[u][a].scale(s), z32 = par[u][a].zero32(s);
+          f32x4_t c;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) c[v] = EXACT ? 0.f : -z32 * xsum[v];
+#pragma unroll
+          for (int j = 0; j < kSteps; ++j) c = mfma_bf16_16x16x32(xp[j], b[a][j], c);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[a][t][v] = fmaf(sc, c[v], acc[a][t][v]);
+        }
+        if (NT > 1) asm volatile("" ::: "memory");  // the next rows' reads take these registers
+      }
+    }
+  }
+  __device__ __forceinline__ void tiles(int wk, int c0, int c1, const char* const (&x)[NT], f32x4_t (&acc)[NB][NT]) {
+    for (int i0 = c0 + wk; i0 < c1; i0 += U * WK) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * WK;
+        if (i < c1) tile(u, x, (uint32_t)(i - c0) * (kW4K * 2), acc);
+        if (i0 + U * WK < c1) fetch(u, min(i + U * WK, c1 - 1));
+      }
+    }
+  }
+};
+
+// `rows` rows (at most 16 NT) of k_tiles tiles through a stream that `start`
+// has begun: `fill(c0, c1, stride)` writes tiles [c0, c1) of them to LDS.  The
+// sums of the wave land in red[wave][block][16-row tile].
+template <int NB, int NT, typename Stream, typename Fill>
+__device__ __forceinline__ void moe_products(Stream& st, int tid, int wk, int w, int k_tiles, int rows, char* lds, int chunk,
+                                             Fill fill) {
+  const int lane = tid & 63, col = lane & 15, h = lane >> 4;
+  const int stride = chunk * kW4K * 2 + 16;
+  const char* x[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) x[t] = lds + min(16 * t + col, rows - 1) * stride + 16 * h;
+  f32x4_t acc[NB][NT];
+#pragma unroll
+  for (int a = 0; a < NB; ++a)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[a][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int c0 = 0; c0 < k_tiles; c0 += chunk) {
+    const int c1 = min(k_tiles, c0 + chunk);
+    if (c0 > 0) {
+      __syncthreads();  // the chunk before has been read
+      st.start(wk, c0, c1);
+    }
+    fill(c0, c1, stride);
+    __syncthreads();
+    st.tiles(wk, c0, c1, x, acc);
+  }
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(lds) + (4 * h) * kMoePad + col;
+#pragma unroll
+  for (int a = 0; a < NB; ++a)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red[((w * NB + a) * NT + t) * 16 * kMoePad + v * kMoePad] = acc[a][t][v];
+  __syncthreads();
+}
+// The sum of WK waves from w0 on, block a, of output c and a token's PARTS rows.
+template <int NB, int NT, int WK, int PARTS>
+__device__ __forceinline__ float moe_sum(const float* red, int w0, int a, int m, int r, int c) {
+  float s = 0.f;
+#pragma unroll
+  for (int q = PARTS - 1; q >= 0; --q) {  // the small parts first
+    const int row = q * m + r;
+#pragma unroll
+    for (int ww = 0; ww < WK; ++ww)
+      s += red[(((w0 + ww) * NB + a) * NT + (row >> 4)) * 16 * kMoePad + (row & 15) * kMoePad + c];
+  }
+  return s;
+}
+// LDS bytes of the waves' sums.
+constexpr int moe_sum_bytes(int waves, int nb, int nt) { return waves * nb * nt * 16 * kMoePad * 4; }
+// An opaque copy of a lane's number, so that nothing that depends on it is held
+// in registers across a loop.
+__device__ __forceinline__ int moe_tid() {
+  int tid = (int)threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  return tid;
 }
 
 // ------------------------------------------------------------ gate and up
@@ -77,6 +175,9 @@ struct MoeUpArgs {
   const float* weights;
   uint16_t* h;
   MoeEntry* table;
+  uint8_t* counted;
+  uint32_t* arrived;
+  int groups;
 };
 
 // act(g) u, each a few float32 roundings from the formula: silu(g) = g / (1 +
@@ -99,16 +200,28 @@ __device__ __forceinline__ void moe_parts(float v, uint16_t (&o)[PARTS]) {
   }
 }
 
-template <typename E, int KIND, int SUB, int WB, int WK, int U>
+template <typename E, int KIND, int SUB, int NT, int WB, int WK, int U>
 __global__ __launch_bounds__(64 * WB * WK) __attribute__((amdgpu_waves_per_eu(2)))
 void moe_up_kernel(const MoeUpArgs p) {
   constexpr int kParts = XFrag<E>::kParts, kHParts = kParts == 1 ? 2 : 3, W = WB * WK;
-  typedef W4Params<KIND, SUB> Par;
+  constexpr int kTokens = 16 * NT / kParts;  // at a time
   extern __shared__ __align__(16) char lds[];  // x; then the waves' sums
   __shared__ uint16_t s_row[LORA_W4_MOE_MAX_TOKENS], s_tok[LORA_W4_MOE_MAX_TOKENS];
-  const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, h = lane >> 4;
+  const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wb = w / WK, wk = w % WK;
 
+  // For the second kernel: nobody has arrived, and the choices that count (an
+  // expert's first in a token).
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    for (int i = tid; i < p.groups; i += 64 * W) p.arrived[i] = 0u;
+    for (int r = tid; r < p.T * p.k; r += 64 * W) {
+      const int id = p.ids[r], r0 = r / p.k * p.k;
+      bool ok = (unsigned)id < (unsigned)p.n;
+#pragma unroll 4
+      for (int i = r0; i < r; ++i) ok = ok && p.ids[i] != id;
+      p.counted[r] = ok;
+    }
+  }
   // ---- the expert's tokens, a token per lane, its weights added up; every
   // wave finds the same
   const int e = p.by_row ? p.ids[blockIdx.y] : (int)blockIdx.y;
@@ -118,8 +231,9 @@ void moe_up_kernel(const MoeUpArgs p) {
 #pragma unroll 8
     for (int j = 0; j < p.k; ++j) {
       const int r = lane * p.k + j;
+      const float wt = p.weights[r];
       if (p.ids[r] == e) {
-        wsum = first < 0 ? p.weights[r] : wsum + p.weights[r];
+        wsum = first < 0 ? wt : wsum + wt;
         first = first < 0 ? r : first;
       }
     }
@@ -128,6 +242,7 @@ void moe_up_kernel(const MoeUpArgs p) {
   int cnt = __popcll(hits);
   // By choice: the first row of an expert works for all of its rows.
   if (cnt > 0 && p.by_row && __builtin_amdgcn_readlane(first, __ffsll((unsigned long long)hits) - 1) != (int)blockIdx.y) cnt = 0;
+  const int at = __popcll(hits & lanemask_lt());
   if (blockIdx.x == 0 && w == 0) {
     MoeEntry& t = p.table[blockIdx.y];
     if (lane == 0) {
@@ -135,96 +250,65 @@ void moe_up_kernel(const MoeUpArgs p) {
       t.cnt = cnt;
     }
     if (cnt > 0 && first >= 0) {
-      const int at = __popcll(hits & lanemask_lt());
       t.row[at] = (uint16_t)first;
       t.tok[at] = (uint16_t)lane;
       t.w[at] = wsum;
     }
   }
   if (cnt == 0) return;
+
+  const int fb = (int)blockIdx.x * WB + wb;  // block of 16 features; from row_tiles on: pads of h
+  const int64_t tile0 = (int64_t)min(fb, p.row_tiles - 1) * p.k_tiles;
+  typedef MoeStream<KIND, SUB, (kParts > 1), 2, NT, WK, U> Stream;
+  const int64_t code_at = e * p.code_stride + tile0 * kW4TileBytes;
+  const int64_t par_at = e * p.param_stride + tile0 * kW4Rows * Stream::Par::kBytes;
+  Stream st;
+  st.code0[0] = p.gate + code_at;
+  st.code0[1] = p.up + code_at;
+  st.par0[0] = p.gate_par + par_at;
+  st.par0[1] = p.up_par + par_at;
+  st.mask = w4_scalar(kCodeMask);
+  st.magic = w4_vector(kMagicBf16);
+  st.lane_code = 16 * lane;
+  st.lane_par = col * Stream::Par::kBytes;
   if (first >= 0) {  // all waves write the same
-    const int at = __popcll(hits & lanemask_lt());
     s_row[at] = (uint16_t)first;
     s_tok[at] = (uint16_t)lane;
   }
-  __syncthreads();
-
-  const int fb = (int)blockIdx.x * WB + wb;  // block of 16 features; from row_tiles on: pads of h
-  const uint32_t mask = w4_scalar(kCodeMask), magic = w4_vector(kMagicBf16);
-  const int64_t tile0 = (int64_t)min(fb, p.row_tiles - 1) * p.k_tiles;
-  const int64_t code_at = e * p.code_stride + tile0 * kW4TileBytes + 16 * lane;
-  const int64_t par_at = e * p.param_stride + tile0 * kW4Rows * Par::kBytes + col * Par::kBytes;
-  const char* code0[2] = {p.gate + code_at, p.up + code_at};
-  const char* par0[2] = {p.gate_par + par_at, p.up_par + par_at};
-
-  for (int m0 = 0; m0 < cnt; m0 += kMoeRows) {
-    const int m = min(kMoeRows, cnt - m0);
+  for (int m0 = 0; m0 < cnt; m0 += kTokens) {
+    const int tid = moe_tid(), m = min(kTokens, cnt - m0), rows = m * kParts;
     // All inputs of the rows in LDS, or as many tiles as fit.
-    const int chunk = min(p.k_tiles, (p.lds_bytes / m - 16) / (kParts * kW4K * 2));
-    const int plane = chunk * kW4K * 2, xrow = kParts * plane + 16;
-    const char* xl = lds + min(col, m - 1) * xrow + 16 * h;
-    f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    for (int c0 = 0; c0 < p.k_tiles; c0 += chunk) {
-      const int c1 = min(p.k_tiles, c0 + chunk);
-      uint4 code[U][2];
-      Par par[U][2];
-      auto fetch = [&](int u, int kt) {
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          code[u][a] = ld16(code0[a] + (int64_t)kt * kW4TileBytes);
-          par[u][a].load(par0[a] + (int64_t)kt * (kW4Rows * Par::kBytes));
-        }
-      };
-#pragma unroll
-      for (int u = 0; u < U; ++u) fetch(u, min(c0 + wk + u * WK, c1 - 1));
-      __syncthreads();  // the chunk (or the sums) before has been read
+    const int chunk = min(p.k_tiles, (p.lds_bytes / rows - 16) / (kW4K * 2));
+    st.start(wk, 0, chunk);
+    __syncthreads();  // the tokens are there; the sums before have been read
+    moe_products<2, NT>(st, tid, wk, w, p.k_tiles, rows, lds, chunk, [&](int c0, int c1, int stride) {
       const int pieces = (c1 - c0) * (kW4K / 8);
       for (int i = tid; i < m * pieces; i += 64 * W) {
-        const int row = i / pieces, at = i - row * pieces, kk = c0 * kW4K + 8 * at;
+        const int r = i / pieces, pc = i - r * pieces, kk = c0 * kW4K + 8 * pc;
         uint4 parts[kParts];
         if (kk < p.d) {
           XFrag<E> f;
-          f.load(p.x + (int64_t)s_tok[m0 + row] * p.ldx_bytes + (int64_t)kk * E::kBytes);
+          f.load(p.x + (int64_t)s_tok[m0 + r] * p.ldx_bytes + (int64_t)kk * E::kBytes);
           f.parts(parts);
         } else {
 #pragma unroll
           for (int q = 0; q < kParts; ++q) parts[q] = make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) st16(lds + row * xrow + q * plane + 16 * at, parts[q]);
+        for (int q = 0; q < kParts; ++q) st16(lds + (q * m + r) * stride + 16 * pc, parts[q]);
       }
-      __syncthreads();
-      for (int i0 = c0 + wk; i0 < c1; i0 += U * WK) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int i = i0 + u * WK;
-          if (i < c1) moe_tile<kParts, (kParts > 1), SUB, 2, Par>(xl + (i - c0) * kW4K * 2, plane, code[u], par[u], mask, magic, acc);
-          if (i0 + U * WK < c1) fetch(u, min(i + U * WK, c1 - 1));
-        }
-      }
-    }
-    // ---- the waves' sums, in wave order; then h
-    __syncthreads();
-    float* red = reinterpret_cast<float*>(lds);
-#pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[(w * 2 + a) * 16 * kMoePad + (4 * h + v) * kMoePad + col] = acc[a][v];
-    __syncthreads();
+    });
+    const float* red = reinterpret_cast<const float*>(lds);
     for (int i = tid; i < WB * 16 * m; i += 64 * W) {
-      const int c = i & 15, b = (i >> 4) % WB, row = (i >> 4) / WB;
-      float g = 0.f, u = 0.f;
-#pragma unroll
-      for (int ww = 0; ww < WK; ++ww) {
-        g += red[((b * WK + ww) * 2) * 16 * kMoePad + row * kMoePad + c];
-        u += red[((b * WK + ww) * 2 + 1) * 16 * kMoePad + row * kMoePad + c];
-      }
+      const int c = i & 15, b = (i >> 4) % WB, r = (i >> 4) / WB;
+      const float g = moe_sum<2, NT, WK, kParts>(red, b * WK, 0, m, r, c);
+      const float u = moe_sum<2, NT, WK, kParts>(red, b * WK, 1, m, r, c);
       const int f = 16 * ((int)blockIdx.x * WB + b) + c, fp = p.h_tiles * kW4K;
       if (f >= fp) continue;
       uint16_t o[kHParts];
       moe_parts<kHParts>(f < p.ffn ? moe_act(p.act, g, u) : 0.f, o);
 #pragma unroll
-      for (int q = 0; q < kHParts; ++q) p.h[((int64_t)s_row[m0 + row] * kHParts + q) * fp + f] = o[q];
+      for (int q = 0; q < kHParts; ++q) p.h[((int64_t)s_row[m0 + r] * kHParts + q) * fp + f] = o[q];
     }
   }
 }
@@ -234,115 +318,119 @@ struct MoeDownArgs {
   const char *codes, *params;
   int64_t code_stride, param_stride;
   int d_out, k_tiles, row_tiles;
-  int T, entries, cap;  // rows of h held in LDS at a time
+  int T, k, lds_bytes;
   const uint16_t* h;
   const MoeEntry* table;
+  float* part;
+  const uint8_t* counted;
+  uint32_t* arrived;
   char* y;
   int64_t ldy_bytes;
 };
 
-constexpr int kMoeItems = 16;  // chunks of an expert's rows that are taken together
+// Values that another workgroup of the kernel reads: stores and loads of the
+// device's scope, which pass by the caches that are not coherent between the
+// XCDs.  A wave's stores have reached memory once it has waited for them; then
+// it may be counted as arrived.  (A fence of that scope writes back all of an
+// XCD's L2: 26 us for the kernel of one token, 8 of 64 experts 1408 -> 2048, and 11 so.)
+__device__ __forceinline__ void moe_publish(float* p, float v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float moe_collect(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void moe_published() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-template <typename E, int KIND, int SUB, int WB, int WE, int U>
-__global__ __launch_bounds__(64 * WB * WE) __attribute__((amdgpu_waves_per_eu(2)))
+// A wave owns NB blocks of 16 outputs.
+template <typename E, int KIND, int SUB, int NT, int NB, int WK, int U>
+__global__ __launch_bounds__(64 * (kMoeDownBlocks / NB) * WK) __attribute__((amdgpu_waves_per_eu(2)))
 void moe_down_kernel(const MoeDownArgs p) {
-  constexpr int kParts = E::kBytes == 2 ? 2 : 3, W = WB * WE;
-  typedef W4Params<KIND, SUB> Par;
-  // The waves' sums [W][T][16], then rows of h.
+  constexpr int kParts = E::kBytes == 2 ? 2 : 3, W = kMoeDownBlocks / NB * WK;
+  constexpr int kTokens = 16 * NT / kParts;
   extern __shared__ __align__(16) char lds[];
-  struct Item {
-    int e, entry, first, m, at;  // expert; its rows first .. + m - 1 of the entry; the first one's place in LDS
-  };
-  __shared__ Item items[kMoeItems];
-  const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, h = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wb = w / WE, we = w % WE;
-  float* sums = reinterpret_cast<float*>(lds);
-  char* rows = lds + W * p.T * 64;
-  const int plane = p.k_tiles * kW4K * 2, hrow = kParts * plane + 16;
-  for (int i = tid; i < W * p.T * 16; i += 64 * W) sums[i] = 0.f;
-  float* mine = sums + w * p.T * 16;
-  const int ob = (int)blockIdx.x * WB + wb;
-  const uint32_t mask = w4_scalar(kCodeMask), magic = w4_vector(kMagicBf16);
-  const int64_t tile0 = (int64_t)min(ob, p.row_tiles - 1) * p.k_tiles;
-  const char* code0 = p.codes + tile0 * kW4TileBytes + 16 * lane;
-  const char* par0 = p.params + tile0 * kW4Rows * Par::kBytes + col * Par::kBytes;
-
-  int at_entry = 0, at_row = 0;  // uniform: the walk through the table
-  while (at_entry < p.entries) {
-    __syncthreads();  // the rows and items before have been read
-    int n_items = 0, used = 0;
-    while (at_entry < p.entries && n_items < kMoeItems && used < p.cap) {
-      const int cnt = p.table[at_entry].cnt, left = cnt - at_row;
-      if (left <= 0) {
-        ++at_entry;
-        at_row = 0;
-        continue;
-      }
-      const int m = min(min(left, kMoeRows), p.cap - used);
-      if (tid == 0) items[n_items] = Item{p.table[at_entry].e, at_entry, at_row, m, used};
-      ++n_items;
-      used += m;
-      at_row += m;
-    }
-    __syncthreads();
-    const int pieces = hrow / 16 - 1;
-    for (int i = tid; i < used * pieces; i += 64 * W) {
-      const int row = i / pieces, at = i - row * pieces;
-      int it = 0;
-      while (it + 1 < n_items && items[it + 1].at <= row) ++it;
-      const int r = p.table[items[it].entry].row[items[it].first + row - items[it].at];
-      st16(rows + row * hrow + 16 * at, ld16(reinterpret_cast<const char*>(p.h) + (int64_t)r * kParts * plane + 16 * at));
-    }
-    __syncthreads();
-    f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-    int cur = -1;
-    auto flush = [&]() {
-      const Item t = items[cur];
+  __shared__ uint16_t s_row[LORA_W4_MOE_MAX_TOKENS];
+  __shared__ float s_w[LORA_W4_MOE_MAX_TOKENS];
+  __shared__ int last;
+  const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wb = w / WK, wk = w % WK;
+  const MoeEntry& t = p.table[blockIdx.y];
+  const int e = t.e, cnt = t.cnt, o0 = (int)blockIdx.x * kMoeDownBlocks * 16;
+  typedef MoeStream<KIND, SUB, (kParts > 2), NB, NT, WK, U> Stream;
+  if (cnt > 0) {
+    Stream st;
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (4 * h + v < t.m) {
-          const int i = t.first + 4 * h + v;
-          float* s = mine + p.table[t.entry].tok[i] * 16 + col;
-          *s = fmaf(p.table[t.entry].w[i], acc[0][v], *s);
+    for (int a = 0; a < NB; ++a) {
+      const int64_t tile0 = (int64_t)min((int)blockIdx.x * kMoeDownBlocks + wb * NB + a, p.row_tiles - 1) * p.k_tiles;
+      st.code0[a] = p.codes + e * p.code_stride + tile0 * kW4TileBytes;
+      st.par0[a] = p.params + e * p.param_stride + tile0 * kW4Rows * Stream::Par::kBytes;
+    }
+    st.mask = w4_scalar(kCodeMask);
+    st.magic = w4_vector(kMagicBf16);
+    st.lane_code = 16 * lane;
+    st.lane_par = col * Stream::Par::kBytes;
+    if (lane < cnt) {  // all waves write the same
+      s_row[lane] = t.row[lane];
+      s_w[lane] = t.w[lane];
+    }
+    const int plane = p.k_tiles * kW4K * 2;
+    for (int m0 = 0; m0 < cnt; m0 += kTokens) {
+      const int tid = moe_tid(), m = min(kTokens, cnt - m0), rows = m * kParts;
+      const int chunk = min(p.k_tiles, (p.lds_bytes / rows - 16) / (kW4K * 2));
+      st.start(wk, 0, chunk);
+      __syncthreads();
+      moe_products<NB, NT>(st, tid, wk, w, p.k_tiles, rows, lds, chunk, [&](int c0, int c1, int stride) {
+        const int pieces = (c1 - c0) * (kW4K / 8);
+        for (int i = tid; i < rows * pieces; i += 64 * W) {
+          const int row = i / pieces, pc = i - row * pieces, q = row / m, r = row - q * m;
+          const char* src = reinterpret_cast<const char*>(p.h) + ((int64_t)s_row[m0 + r] * kParts + q) * plane;
+          st16(lds + row * stride + 16 * pc, ld16(src + c0 * (kW4K * 2) + 16 * pc));
         }
-      acc[0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    };
-    const int tiles = n_items * p.k_tiles;
-    for (int i = we; i < tiles; i += WE) {
-      const int it = i / p.k_tiles, kt = i - it * p.k_tiles;
-      if (it != cur) {
-        if (cur >= 0) flush();
-        cur = it;
+      });
+      const float* red = reinterpret_cast<const float*>(lds);
+      for (int i = tid; i < kMoeDownBlocks * 16 * m; i += 64 * W) {
+        const int c = i & 15, b = (i >> 4) % kMoeDownBlocks, r = (i >> 4) / kMoeDownBlocks, o = o0 + 16 * b + c;
+        if (o < p.d_out)
+          moe_publish(p.part + (int64_t)s_row[m0 + r] * p.d_out + o,
+                      s_w[m0 + r] * moe_sum<NB, NT, WK, kParts>(red, b / NB * WK, b % NB, m, r, c));
       }
-      const Item t = items[it];
-      uint4 code[1] = {ld16(code0 + t.e * p.code_stride + (int64_t)kt * kW4TileBytes)};
-      Par par[1];
-      par[0].load(par0 + t.e * p.param_stride + (int64_t)kt * (kW4Rows * Par::kBytes));
-      const char* x = rows + (t.at + min(col, t.m - 1)) * hrow + 16 * h + kt * kW4K * 2;
-      moe_tile<kParts, (kParts > 2), SUB, 1, Par>(x, plane, code, par, mask, magic, acc);
     }
-    if (cur >= 0) flush();
+    moe_published();
   }
+  // ---- the last workgroup of these outputs adds the choices' rows
   __syncthreads();
-  for (int i = tid; i < WB * 16 * p.T; i += 64 * W) {
-    const int c = i & 15, b = (i >> 4) % WB, t = (i >> 4) / WB;
-    const int o = 16 * ((int)blockIdx.x * WB + b) + c;
+  if (tid == 0)
+    last = __hip_atomic_fetch_add(&p.arrived[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.y - 1;
+  __syncthreads();
+  if (!last) return;
+  for (int i = tid; i < p.T * kMoeDownBlocks * 4; i += 64 * W) {
+    const int tok = i / (kMoeDownBlocks * 4), o = o0 + 4 * (i % (kMoeDownBlocks * 4));
     if (o >= p.d_out) continue;
-    float s = 0.f;
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int j = 0; j < p.k; ++j) {
+      const int64_t r = (int64_t)tok * p.k + j;
+      if (p.counted[r]) {
 #pragma unroll
-    for (int ww = 0; ww < WE; ++ww) s += sums[((b * WE + ww) * p.T + t) * 16 + c];
-    char* dst = p.y + (int64_t)t * p.ldy_bytes;
-    if constexpr (E::kBytes == 2) reinterpret_cast<uint16_t*>(dst)[o] = (uint16_t)f32_to_bf16(s);
-    else reinterpret_cast<float*>(dst)[o] = s;
+        for (int v = 0; v < 4; ++v) s[v] += moe_collect(p.part + r * p.d_out + o + v);
+      }
+    }
+    char* dst = p.y + (int64_t)tok * p.ldy_bytes + (int64_t)o * E::kBytes;
+    if constexpr (E::kBytes == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+    else *reinterpret_cast<f32x4_t*>(dst) = s;
   }
 }
 
-constexpr int kMoeLds = 64 * 1024;  // of rows
+// LDS of a call: the rows of as many tokens as come together, up to kMoeLds,
+// and the waves' sums.
+inline int moe_lds_bytes(int T, int parts, int nt, int k_tiles, int sums) {
+  const int at_once = 16 * nt / parts;
+  const int64_t rows = (int64_t)(T < at_once ? T : at_once) * parts * ((int64_t)k_tiles * kW4K * 2 + 16);
+  const int64_t some = rows > kMoeLds ? kMoeLds : rows;
+  return (int)(some > sums ? some : sums);
+}
 
-template <typename E, int KIND, int SUB>
-hipError_t launch_up(const MoeCall& c, hipStream_t stream) {
-  constexpr int WB = 2, WK = 4, U = 2;
-  constexpr int kParts = XFrag<E>::kParts;
+template <typename E, int KIND, int SUB, int NT, int WB, int WK, int U>
+hipError_t run_up(const MoeCall& c, hipStream_t stream) {
   MoeUpArgs a{};
   a.gate = reinterpret_cast<const char*>(c.gate.codes);
   a.gate_par = reinterpret_cast<const char*>(c.gate.params);
@@ -366,22 +454,21 @@ hipError_t launch_up(const MoeCall& c, hipStream_t stream) {
   a.weights = c.weights;
   a.h = reinterpret_cast<uint16_t*>(c.ws + c.plan.h);
   a.table = reinterpret_cast<MoeEntry*>(c.ws + c.plan.table);
-  const int64_t row = (int64_t)kParts * a.k_tiles * kW4K * 2 + 16;
-  const int64_t all = (c.T < kMoeRows ? c.T : kMoeRows) * row;
-  const int64_t sums = (int64_t)WB * WK * 2 * 16 * kMoePad * 4;
-  a.lds_bytes = (int)(all < kMoeLds ? (all > sums ? all : sums) : kMoeLds);
+  a.counted = reinterpret_cast<uint8_t*>(c.ws + c.plan.counted);
+  a.arrived = reinterpret_cast<uint32_t*>(c.ws + c.plan.arrived);
+  a.groups = moe_down_groups(c.down.d_out);
+  a.lds_bytes = moe_lds_bytes(c.T, XFrag<E>::kParts, NT, a.k_tiles, moe_sum_bytes(WB * WK, 2, NT));
   static DynLdsLimit lim;
-  const hipError_t e = ensure_dynamic_lds(lim, reinterpret_cast<const void*>(moe_up_kernel<E, KIND, SUB, WB, WK, U>), (size_t)a.lds_bytes);
+  const auto kernel = moe_up_kernel<E, KIND, SUB, NT, WB, WK, U>;
+  const hipError_t e = ensure_dynamic_lds(lim, reinterpret_cast<const void*>(kernel), (size_t)a.lds_bytes);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((a.h_tiles * 8 + WB - 1) / WB), (unsigned)c.plan.entries);
-  hipLaunchKernelGGL((moe_up_kernel<E, KIND, SUB, WB, WK, U>), grid, dim3(64 * WB * WK), (size_t)a.lds_bytes, stream, a);
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * WB * WK), (size_t)a.lds_bytes, stream, a);
   return hipGetLastError();
 }
 
-template <typename E, int KIND, int SUB>
-hipError_t launch_down(const MoeCall& c, hipStream_t stream) {
-  constexpr int WB = 1, WE = 8, U = 2;
-  constexpr int kParts = E::kBytes == 2 ? 2 : 3;
+template <typename E, int KIND, int SUB, int NT, int NB, int WK, int U>
+hipError_t run_down(const MoeCall& c, hipStream_t stream) {
   MoeDownArgs a{};
   a.codes = reinterpret_cast<const char*>(c.down.codes);
   a.params = reinterpret_cast<const char*>(c.down.params);
@@ -391,24 +478,39 @@ hipError_t launch_down(const MoeCall& c, hipStream_t stream) {
   a.k_tiles = c.plan.h_tiles;
   a.row_tiles = w4_row_tiles(a.d_out);
   a.T = c.T;
-  a.entries = c.plan.entries;
+  a.k = c.k;
   a.h = reinterpret_cast<const uint16_t*>(c.ws + c.plan.h);
   a.table = reinterpret_cast<const MoeEntry*>(c.ws + c.plan.table);
+  a.part = reinterpret_cast<float*>(c.ws + c.plan.part);
+  a.counted = reinterpret_cast<const uint8_t*>(c.ws + c.plan.counted);
+  a.arrived = reinterpret_cast<uint32_t*>(c.ws + c.plan.arrived);
   a.y = reinterpret_cast<char*>(c.y);
   a.ldy_bytes = c.ldy * E::kBytes;
-  const int64_t row = (int64_t)kParts * a.k_tiles * kW4K * 2 + 16;
-  const int64_t sums = (int64_t)WB * WE * c.T * 64;
-  int64_t cap = kMoeLds / row;
-  cap = cap < 1 ? 1 : (cap > (int64_t)c.T * c.k ? (int64_t)c.T * c.k : cap);
-  a.cap = (int)cap;
-  const int64_t lds = sums + cap * row;
-  if (lds > 150 * 1024) return hipErrorInvalidValue;
+  a.lds_bytes = moe_lds_bytes(c.T, moe_h_parts(c.dtype), NT, a.k_tiles, moe_sum_bytes(kMoeDownBlocks / NB * WK, NB, NT));
   static DynLdsLimit lim;
-  const hipError_t e = ensure_dynamic_lds(lim, reinterpret_cast<const void*>(moe_down_kernel<E, KIND, SUB, WB, WE, U>), (size_t)lds);
+  const auto kernel = moe_down_kernel<E, KIND, SUB, NT, NB, WK, U>;
+  const hipError_t e = ensure_dynamic_lds(lim, reinterpret_cast<const void*>(kernel), (size_t)a.lds_bytes);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_down_kernel<E, KIND, SUB, WB, WE, U>), dim3((unsigned)((a.row_tiles + WB - 1) / WB)), dim3(64 * WB * WE),
-                     (size_t)lds, stream, a);
+  const dim3 grid((unsigned)moe_down_groups(a.d_out), (unsigned)c.plan.entries);
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * kMoeDownBlocks / NB * WK), (size_t)a.lds_bytes, stream, a);
   return hipGetLastError();
+}
+
+// Two 16-row tiles where an expert has more tokens, on average, than about half
+// of what one holds.
+inline bool moe_two_tiles(const MoeCall& c, int parts) {
+  return c.T > 16 / parts && 2 * c.T * c.k * parts > 16 * c.gate.n;
+}
+
+template <typename E, int KIND, int SUB>
+hipError_t launch_up(const MoeCall& c, hipStream_t stream) {
+  if (moe_two_tiles(c, XFrag<E>::kParts)) return run_up<E, KIND, SUB, 2, 2, 4, 2>(c, stream);
+  return run_up<E, KIND, SUB, 1, 2, 4, 2>(c, stream);
+}
+template <typename E, int KIND, int SUB>
+hipError_t launch_down(const MoeCall& c, hipStream_t stream) {
+  if (moe_two_tiles(c, moe_h_parts(c.dtype))) return run_down<E, KIND, SUB, 2, 2, 2, 2>(c, stream);
+  return run_down<E, KIND, SUB, 1, 2, 2, 2>(c, stream);
 }
 
 template <typename E, bool UP>
