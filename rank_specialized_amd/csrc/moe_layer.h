@@ -104,12 +104,40 @@ struct MoeStream {
   }
 };
 
+// Tiles of `rows` rows that LDS holds at a time.
+__device__ __forceinline__ int moe_chunk(int lds_bytes, int rows, int k_tiles) {
+  return min(k_tiles, (lds_bytes / rows - 16) / (kW4K * 2));
+}
+// An LDS barrier behind every load that the wave has asked for.
+__device__ __forceinline__ void moe_loads_barrier() {
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+// Tiles [c0, c1) of rows of bf16 numbers into LDS by loads that write it
+// directly, all of them in flight at once; row i from src(i), which is uniform.
+// A wave-wide load takes four tiles of a row, pieces from `pieces` on repeat the
+// one before.
+template <int W, typename Src>
+__device__ __forceinline__ void moe_dma(char* lds, int stride, int rows, int c0, int c1, int pieces, int w, int lane, Src src) {
+  const int per_row = (c1 - c0 + 3) >> 2;
+  for (int row = 0, f = w; row < rows; ++row, f -= per_row)
+    for (; f < per_row; f += W)
+      if (64 * f + lane < 16 * (c1 - c0)) {
+        const uint32_t at = (uint32_t)min(16 * c0 + 64 * f + lane, pieces - 1) * 16;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src(row) + at),
+                                         (__attribute__((address_space(3))) void*)(lds + row * stride + f * 1024), 16, 0, 0);
+      }
+}
+
 // `rows` rows (at most 16 NT) of k_tiles tiles through a stream that `start`
-// has begun: `fill(c0, c1, stride)` writes tiles [c0, c1) of them to LDS.  The
-// sums of the wave land in red[wave][block][16-row tile].
-template <int NB, int NT, typename Stream, typename Fill>
+// has begun: `fill(c0, c1, stride)` asks for tiles [c0, c1) of them to be
+// written to LDS, `ends(c0, stride)` clears what lies behind a row's end in the
+// last of them (`ragged`).  The sums of the wave land in red[wave][block][16-row
+// tile].
+template <int NB, int NT, typename Stream, typename Fill, typename Ends>
 __device__ __forceinline__ void moe_products(Stream& st, int tid, int wk, int w, int k_tiles, int rows, char* lds, int chunk,
-                                             Fill fill) {
+                                             bool ragged, Fill fill, Ends ends) {
   const int lane = tid & 63, col = lane & 15, h = lane >> 4;
   const int stride = chunk * kW4K * 2 + 16;
   const char* x[NT];
@@ -127,7 +155,11 @@ __device__ __forceinline__ void moe_products(Stream& st, int tid, int wk, int w,
       st.start(wk, c0, c1);
     }
     fill(c0, c1, stride);
-    __syncthreads();
+    moe_loads_barrier();
+    if (ragged && c1 == k_tiles) {
+      ends(c0, stride);
+      __syncthreads();
+    }
     st.tiles(wk, c0, c1, x, acc);
   }
   __syncthreads();
@@ -210,6 +242,25 @@ void moe_up_kernel(const MoeUpArgs p) {
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wb = w / WK, wk = w % WK;
 
+  // ---- the first codes are asked for before the expert's tokens are known
+  const int e = p.by_row ? p.ids[blockIdx.y] : (int)blockIdx.y, e0 = (unsigned)e < (unsigned)p.n ? e : 0;
+  const int fb = (int)blockIdx.x * WB + wb;  // block of 16 features; from row_tiles on: pads of h
+  const int64_t tile0 = (int64_t)min(fb, p.row_tiles - 1) * p.k_tiles;
+  typedef MoeStream<KIND, SUB, (kParts > 1), 2, NT, WK, U> Stream;
+  const int64_t code_at = e0 * p.code_stride + tile0 * kW4TileBytes;
+  const int64_t par_at = e0 * p.param_stride + tile0 * kW4Rows * Stream::Par::kBytes;
+  Stream st;
+  st.code0[0] = p.gate + code_at;
+  st.code0[1] = p.up + code_at;
+  st.par0[0] = p.gate_par + par_at;
+  st.par0[1] = p.up_par + par_at;
+  st.mask = w4_scalar(kCodeMask);
+  st.magic = w4_vector(kMagicBf16);
+  st.lane_code = 16 * lane;
+  st.lane_par = col * Stream::Par::kBytes;
+  st.start(wk, 0, p.k_tiles);
+  asm volatile("" ::: "memory");
+
   // For the second kernel: nobody has arrived, and the choices that count (an
   // expert's first in a token).
   if (blockIdx.x == 0 && blockIdx.y == 0) {
@@ -224,7 +275,6 @@ void moe_up_kernel(const MoeUpArgs p) {
   }
   // ---- the expert's tokens, a token per lane, its weights added up; every
   // wave finds the same
-  const int e = p.by_row ? p.ids[blockIdx.y] : (int)blockIdx.y;
   int first = -1;
   float wsum = 0.f;
   if (lane < p.T) {
@@ -257,47 +307,51 @@ void moe_up_kernel(const MoeUpArgs p) {
   }
   if (cnt == 0) return;
 
-  const int fb = (int)blockIdx.x * WB + wb;  // block of 16 features; from row_tiles on: pads of h
-  const int64_t tile0 = (int64_t)min(fb, p.row_tiles - 1) * p.k_tiles;
-  typedef MoeStream<KIND, SUB, (kParts > 1), 2, NT, WK, U> Stream;
-  const int64_t code_at = e * p.code_stride + tile0 * kW4TileBytes;
-  const int64_t par_at = e * p.param_stride + tile0 * kW4Rows * Stream::Par::kBytes;
-  Stream st;
-  st.code0[0] = p.gate + code_at;
-  st.code0[1] = p.up + code_at;
-  st.par0[0] = p.gate_par + par_at;
-  st.par0[1] = p.up_par + par_at;
-  st.mask = w4_scalar(kCodeMask);
-  st.magic = w4_vector(kMagicBf16);
-  st.lane_code = 16 * lane;
-  st.lane_par = col * Stream::Par::kBytes;
   if (first >= 0) {  // all waves write the same
     s_row[at] = (uint16_t)first;
     s_tok[at] = (uint16_t)lane;
   }
+  __syncthreads();
   for (int m0 = 0; m0 < cnt; m0 += kTokens) {
     const int tid = moe_tid(), m = min(kTokens, cnt - m0), rows = m * kParts;
-    // All inputs of the rows in LDS, or as many tiles as fit.
-    const int chunk = min(p.k_tiles, (p.lds_bytes / rows - 16) / (kW4K * 2));
-    st.start(wk, 0, chunk);
-    __syncthreads();  // the tokens are there; the sums before have been read
-    moe_products<2, NT>(st, tid, wk, w, p.k_tiles, rows, lds, chunk, [&](int c0, int c1, int stride) {
-      const int pieces = (c1 - c0) * (kW4K / 8);
-      for (int i = tid; i < m * pieces; i += 64 * W) {
-        const int r = i / pieces, pc = i - r * pieces, kk = c0 * kW4K + 8 * pc;
-        uint4 parts[kParts];
-        if (kk < p.d) {
-          XFrag<E> f;
-          f.load(p.x + (int64_t)s_tok[m0 + r] * p.ldx_bytes + (int64_t)kk * E::kBytes);
-          f.parts(parts);
-        } else {
+    const int chunk = moe_chunk(p.lds_bytes, rows, p.k_tiles);
+    if (m0 > 0) {
+      __syncthreads();  // the sums before have been read
+      st.start(wk, 0, chunk);
+    }
+    moe_products<2, NT>(
+        st, tid, wk, w, p.k_tiles, rows, lds, chunk, p.d % kW4K != 0,
+        [&](int c0, int c1, int stride) {
+          if constexpr (kParts == 1) {
+            moe_dma<W>(lds, stride, m, c0, c1, p.d / 8, w, tid & 63, [&](int r) {
+              return p.x + (int64_t)__builtin_amdgcn_readfirstlane((int)s_tok[m0 + r]) * p.ldx_bytes;
+            });
+          } else {
+            constexpr int kBatch = 4;  // pieces in flight per lane
+            const int pieces = (c1 - c0) * (kW4K / 8), total = m * pieces;
+            for (int i0 = tid; i0 < total; i0 += 64 * W * kBatch) {
+              XFrag<E> f[kBatch];
 #pragma unroll
-          for (int q = 0; q < kParts; ++q) parts[q] = make_uint4(0u, 0u, 0u, 0u);
-        }
+              for (int b = 0; b < kBatch; ++b) {
+                const int i = min(i0 + 64 * W * b, total - 1), r = (int)((uint32_t)i / (uint32_t)pieces), pc = i - r * pieces;
+                f[b].load(p.x + (int64_t)s_tok[m0 + r] * p.ldx_bytes + (int64_t)min(c0 * kW4K + 8 * pc, p.d - 8) * E::kBytes);
+              }
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) st16(lds + (q * m + r) * stride + 16 * pc, parts[q]);
-      }
-    });
+              for (int b = 0; b < kBatch; ++b) {
+                const int i = min(i0 + 64 * W * b, total - 1), r = (int)((uint32_t)i / (uint32_t)pieces), pc = i - r * pieces;
+                uint4 parts[kParts];
+                f[b].parts(parts);
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) st16(lds + (q * m + r) * stride + 16 * pc, parts[q]);
+              }
+            }
+          }
+        },
+        [&](int c0, int stride) {
+          const int pads = (kW4K - p.d % kW4K) / 8;  // 16-byte pieces
+          for (int i = tid; i < rows * pads; i += 64 * W)
+            st16(lds + i / pads * stride + (p.k_tiles - c0) * kW4K * 2 - 16 * (1 + i % pads), make_uint4(0u, 0u, 0u, 0u));
+        });
     const float* red = reinterpret_cast<const float*>(lds);
     for (int i = tid; i < WB * 16 * m; i += 64 * W) {
       const int c = i & 15, b = (i >> 4) % WB, r = (i >> 4) / WB;
@@ -356,6 +410,8 @@ void moe_down_kernel(const MoeDownArgs p) {
   const MoeEntry& t = p.table[blockIdx.y];
   const int e = t.e, cnt = t.cnt, o0 = (int)blockIdx.x * kMoeDownBlocks * 16;
   typedef MoeStream<KIND, SUB, (kParts > 2), NB, NT, WK, U> Stream;
+  const int my_row = t.row[lane];  // behind cnt: not used
+  const float my_w = t.w[lane];
   if (cnt > 0) {
     Stream st;
 #pragma unroll
@@ -368,24 +424,30 @@ void moe_down_kernel(const MoeDownArgs p) {
     st.magic = w4_vector(kMagicBf16);
     st.lane_code = 16 * lane;
     st.lane_par = col * Stream::Par::kBytes;
+    st.start(wk, 0, p.k_tiles);
+    asm volatile("" ::: "memory");
     if (lane < cnt) {  // all waves write the same
-      s_row[lane] = t.row[lane];
-      s_w[lane] = t.w[lane];
+      s_row[lane] = (uint16_t)my_row;
+      s_w[lane] = my_w;
     }
+    __syncthreads();
     const int plane = p.k_tiles * kW4K * 2;
     for (int m0 = 0; m0 < cnt; m0 += kTokens) {
       const int tid = moe_tid(), m = min(kTokens, cnt - m0), rows = m * kParts;
-      const int chunk = min(p.k_tiles, (p.lds_bytes / rows - 16) / (kW4K * 2));
-      st.start(wk, 0, chunk);
-      __syncthreads();
-      moe_products<NB, NT>(st, tid, wk, w, p.k_tiles, rows, lds, chunk, [&](int c0, int c1, int stride) {
-        const int pieces = (c1 - c0) * (kW4K / 8);
-        for (int i = tid; i < rows * pieces; i += 64 * W) {
-          const int row = i / pieces, pc = i - row * pieces, q = row / m, r = row - q * m;
-          const char* src = reinterpret_cast<const char*>(p.h) + ((int64_t)s_row[m0 + r] * kParts + q) * plane;
-          st16(lds + row * stride + 16 * pc, ld16(src + c0 * (kW4K * 2) + 16 * pc));
-        }
-      });
+      const int chunk = moe_chunk(p.lds_bytes, rows, p.k_tiles);
+      if (m0 > 0) {
+        __syncthreads();
+        st.start(wk, 0, chunk);
+      }
+      moe_products<NB, NT>(
+          st, tid, wk, w, p.k_tiles, rows, lds, chunk, false,
+          [&](int c0, int c1, int stride) {
+            moe_dma<W>(lds, stride, rows, c0, c1, 16 * p.k_tiles, w, tid & 63, [&](int i) {
+              const int q = i / m, r = __builtin_amdgcn_readfirstlane((int)s_row[m0 + i - q * m]);
+              return reinterpret_cast<const char*>(p.h) + ((int64_t)r * kParts + q) * plane;
+            });
+          },
+          [&](int, int) {});
       const float* red = reinterpret_cast<const float*>(lds);
       for (int i = tid; i < kMoeDownBlocks * 16 * m; i += 64 * W) {
         const int c = i & 15, b = (i >> 4) % kMoeDownBlocks, r = (i >> 4) / kMoeDownBlocks, o = o0 + 16 * b + c;
