@@ -10,7 +10,7 @@ namespace lora {
 // weight (the sum of them, where a token names an expert twice).
 struct MoeEntry {
   int32_t e, cnt;
-  uint16_t row[LORA_W4_MOE_MAX_TOKENS], tok[LORA_W4_MOE_MAX_TOKENS];
+  uint16_t row[LORA_W4_MOE_MAX_TOKENS];
   float w[LORA_W4_MOE_MAX_TOKENS];
 };
 

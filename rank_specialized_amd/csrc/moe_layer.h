@@ -28,6 +28,7 @@
 namespace lora {
 namespace {
 
+constexpr int kMoeIds = 8;           // 64 choices each that a wave looks through in registers
 constexpr int kMoePad = 17;          // LDS row stride of a 16 x 16 block of sums
 constexpr int kMoeLds = 76 * 1024;   // of rows: two workgroups to a compute unit
 
@@ -239,11 +240,18 @@ void moe_up_kernel(const MoeUpArgs p) {
   constexpr int kTokens = 16 * NT / kParts;  // at a time
   extern __shared__ __align__(16) char lds[];  // x; then the waves' sums
   __shared__ uint16_t s_row[LORA_W4_MOE_MAX_TOKENS], s_tok[LORA_W4_MOE_MAX_TOKENS];
+  __shared__ float s_sum[LORA_W4_MOE_MAX_TOKENS];
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wb = w / WK, wk = w % WK;
 
-  // ---- the first codes are asked for before the expert's tokens are known
+  // ---- asked for in the order they are waited for: the choices, then the
+  // expert's first codes
+  const int R = p.T * p.k;
+  int id[kMoeIds];
+#pragma unroll
+  for (int i = 0; i < kMoeIds; ++i) id[i] = p.ids[min(64 * i + lane, R - 1)];
   const int e = p.by_row ? p.ids[blockIdx.y] : (int)blockIdx.y, e0 = (unsigned)e < (unsigned)p.n ? e : 0;
+  asm volatile("" ::: "memory");
   const int fb = (int)blockIdx.x * WB + wb;  // block of 16 features; from row_tiles on: pads of h
   const int64_t tile0 = (int64_t)min(fb, p.row_tiles - 1) * p.k_tiles;
   typedef MoeStream<KIND, SUB, (kParts > 1), 2, NT, WK, U> Stream;
@@ -261,57 +269,78 @@ void moe_up_kernel(const MoeUpArgs p) {
   st.start(wk, 0, p.k_tiles);
   asm volatile("" ::: "memory");
 
-  // For the second kernel: nobody has arrived, and the choices that count (an
-  // expert's first in a token).
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    for (int i = tid; i < p.groups; i += 64 * W) p.arrived[i] = 0u;
-    for (int r = tid; r < p.T * p.k; r += 64 * W) {
-      const int id = p.ids[r], r0 = r / p.k * p.k;
-      bool ok = (unsigned)id < (unsigned)p.n;
-#pragma unroll 4
-      for (int i = r0; i < r; ++i) ok = ok && p.ids[i] != id;
-      p.counted[r] = ok;
-    }
-  }
-  // ---- the expert's tokens, a token per lane, its weights added up; every
-  // wave finds the same
-  int first = -1;
+  // ---- the expert's tokens, in order; every wave finds the same, and reads
+  // what it has written itself
+  int cnt = 0, first_row = -1;
   float wsum = 0.f;
-  if (lane < p.T) {
-#pragma unroll 8
-    for (int j = 0; j < p.k; ++j) {
-      const int r = lane * p.k + j;
-      const float wt = p.weights[r];
-      if (p.ids[r] == e) {
-        wsum = first < 0 ? wt : wsum + wt;
-        first = first < 0 ? r : first;
-      }
+  bool plain = R <= 64 * kMoeIds;  // every token names the expert once
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < kMoeIds; ++i) {
+      const int r = 64 * i + lane;
+      const uint64_t hits = __ballot(r < R && id[i] == e);
+      const int at = cnt + __popcll(hits & lanemask_lt());
+      if (((hits >> lane) & 1) && at < LORA_W4_MOE_MAX_TOKENS) s_row[at] = (uint16_t)r;
+      cnt += __popcll(hits);
     }
+    plain = cnt <= LORA_W4_MOE_MAX_TOKENS;
+    if (plain && lane < cnt) {
+      first_row = s_row[lane];
+      const int tok = first_row / p.k;
+      s_tok[lane] = (uint16_t)tok;
+      plain = lane == 0 || (int)s_row[lane - 1] / p.k != tok;
+    }
+    plain = __all(plain);
+    if (plain && blockIdx.x == 0 && lane < cnt) wsum = p.weights[first_row];
   }
-  const uint64_t hits = (unsigned)e < (unsigned)p.n ? __ballot(first >= 0) : 0ull;
-  int cnt = __popcll(hits);
+  if (!plain) {  // a token per lane, its weights added up
+    __syncthreads();  // no wave writes the list above any more
+    int first = -1;
+    if (lane < p.T)
+      for (int r = lane * p.k; r < (lane + 1) * p.k; ++r)
+        if (p.ids[r] == e) {
+          wsum = first < 0 ? p.weights[r] : wsum + p.weights[r];
+          first = first < 0 ? r : first;
+        }
+    const uint64_t hits = __ballot(first >= 0);
+    cnt = __popcll(hits);
+    // Into the first lanes, through LDS.
+    const int at = __popcll(hits & lanemask_lt());
+    if (first >= 0) {
+      s_row[at] = (uint16_t)first;
+      s_tok[at] = (uint16_t)lane;
+      s_sum[at] = wsum;
+    }
+    first_row = lane < cnt ? s_row[lane] : -1;
+    wsum = lane < cnt ? s_sum[lane] : 0.f;
+  }
+  if ((unsigned)e >= (unsigned)p.n) cnt = 0;
   // By choice: the first row of an expert works for all of its rows.
-  if (cnt > 0 && p.by_row && __builtin_amdgcn_readlane(first, __ffsll((unsigned long long)hits) - 1) != (int)blockIdx.y) cnt = 0;
-  const int at = __popcll(hits & lanemask_lt());
+  if (cnt > 0 && p.by_row && __builtin_amdgcn_readfirstlane(first_row) != (int)blockIdx.y) cnt = 0;
   if (blockIdx.x == 0 && w == 0) {
     MoeEntry& t = p.table[blockIdx.y];
     if (lane == 0) {
       t.e = e;
       t.cnt = cnt;
     }
-    if (cnt > 0 && first >= 0) {
-      t.row[at] = (uint16_t)first;
-      t.tok[at] = (uint16_t)lane;
-      t.w[at] = wsum;
+    if (lane < cnt) {
+      t.row[lane] = (uint16_t)first_row;
+      t.w[lane] = wsum;
+    }
+  }
+  // For the second kernel: nobody has arrived, and the choices that count (an
+  // expert's first in a token).
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) {
+    for (int i = tid; i < p.groups; i += 64 * W) p.arrived[i] = 0u;
+    for (int r = tid; r < R; r += 64 * W) {
+      const int own = p.ids[r], r0 = r / p.k * p.k;
+      bool ok = (unsigned)own < (unsigned)p.n;
+#pragma unroll 4
+      for (int i = r0; i < r; ++i) ok = ok && p.ids[i] != own;
+      p.counted[r] = ok;
     }
   }
   if (cnt == 0) return;
-
-  if (first >= 0) {  // all waves write the same
-    s_row[at] = (uint16_t)first;
-    s_tok[at] = (uint16_t)lane;
-  }
-  __syncthreads();
   for (int m0 = 0; m0 < cnt; m0 += kTokens) {
     const int tid = moe_tid(), m = min(kTokens, cnt - m0), rows = m * kParts;
     const int chunk = moe_chunk(p.lds_bytes, rows, p.k_tiles);
@@ -426,11 +455,10 @@ void moe_down_kernel(const MoeDownArgs p) {
     st.lane_par = col * Stream::Par::kBytes;
     st.start(wk, 0, p.k_tiles);
     asm volatile("" ::: "memory");
-    if (lane < cnt) {  // all waves write the same
+    if (lane < cnt) {  // all waves write the same, and read what they have written
       s_row[lane] = (uint16_t)my_row;
       s_w[lane] = my_w;
     }
-    __syncthreads();
     const int plane = p.k_tiles * kW4K * 2;
     for (int m0 = 0; m0 < cnt; m0 += kTokens) {
       const int tid = moe_tid(), m = min(kTokens, cnt - m0), rows = m * kParts;
