@@ -28,7 +28,7 @@ struct MoePlan {
   bool by_row;
   int h_tiles;       // tiles of 128 of a row of h
   size_t h, table;   // h [T k][parts][h_tiles * 128] bf16
-  size_t part;       // [T k][d_out] float32: the choices' weighted outputs
+  size_t part;       // [moe_down_groups][T k][16 kMoeDownBlocks] float32: the choices' weighted outputs
   size_t counted;    // [T k] bytes: whether a choice has such a row
   size_t arrived;    // [moe_down_groups] workgroups that have written theirs
   size_t ws_bytes;
@@ -48,7 +48,7 @@ inline MoePlan moe_plan_call(int n, int ffn, int d_out, int dtype, int T, int k)
   };
   p.h = take((size_t)R * (size_t)moe_h_parts(dtype) * (size_t)p.h_tiles * kW4K * 2);
   p.table = take((size_t)p.entries * sizeof(MoeEntry));
-  p.part = take((size_t)R * (size_t)d_out * 4);
+  p.part = take((size_t)moe_down_groups(d_out) * (size_t)R * 16 * kMoeDownBlocks * 4);
   p.counted = take((size_t)R);
   p.arrived = take((size_t)moe_down_groups(d_out) * 4);
   return p;

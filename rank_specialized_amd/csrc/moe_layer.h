@@ -210,7 +210,7 @@ struct MoeUpArgs {
   MoeEntry* table;
   uint8_t* counted;
   uint32_t* arrived;
-  int groups;
+  int groups, entries;
 };
 
 // act(g) u, each a few float32 roundings from the formula: silu(g) = g / (1 +
@@ -234,7 +234,7 @@ __device__ __forceinline__ void moe_parts(float v, uint16_t (&o)[PARTS]) {
 }
 
 template <typename E, int KIND, int SUB, int NT, int WB, int WK, int U>
-__global__ __launch_bounds__(64 * WB * WK) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ __launch_bounds__(64 * WB * WK) __attribute__((amdgpu_waves_per_eu(NT == 1 ? 4 : 2)))
 void moe_up_kernel(const MoeUpArgs p) {
   constexpr int kParts = XFrag<E>::kParts, kHParts = kParts == 1 ? 2 : 3, W = WB * WK;
   constexpr int kTokens = 16 * NT / kParts;  // at a time
@@ -244,9 +244,23 @@ void moe_up_kernel(const MoeUpArgs p) {
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wb = w / WK, wk = w % WK;
 
+  const int R = p.T * p.k;
+  if ((int)blockIdx.y == p.entries) {
+    // For the second kernel: nobody has arrived, and the choices that count (an
+    // expert's first in a token).
+    if (blockIdx.x > 0) return;
+    for (int i = tid; i < p.groups; i += 64 * W) p.arrived[i] = 0u;
+    for (int r = tid; r < R; r += 64 * W) {
+      const int own = p.ids[r], r0 = r / p.k * p.k;
+      bool ok = (unsigned)own < (unsigned)p.n;
+#pragma unroll 4
+      for (int i = r0; i < r; ++i) ok = ok && p.ids[i] != own;
+      p.counted[r] = ok;
+    }
+    return;
+  }
   // ---- asked for in the order they are waited for: the choices, then the
   // expert's first codes
-  const int R = p.T * p.k;
   int id[kMoeIds];
 #pragma unroll
   for (int i = 0; i < kMoeIds; ++i) id[i] = p.ids[min(64 * i + lane, R - 1)];
@@ -328,18 +342,6 @@ void moe_up_kernel(const MoeUpArgs p) {
       t.w[lane] = wsum;
     }
   }
-  // For the second kernel: nobody has arrived, and the choices that count (an
-  // expert's first in a token).
-  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) {
-    for (int i = tid; i < p.groups; i += 64 * W) p.arrived[i] = 0u;
-    for (int r = tid; r < R; r += 64 * W) {
-      const int own = p.ids[r], r0 = r / p.k * p.k;
-      bool ok = (unsigned)own < (unsigned)p.n;
-#pragma unroll 4
-      for (int i = r0; i < r; ++i) ok = ok && p.ids[i] != own;
-      p.counted[r] = ok;
-    }
-  }
   if (cnt == 0) return;
   for (int m0 = 0; m0 < cnt; m0 += kTokens) {
     const int tid = moe_tid(), m = min(kTokens, cnt - m0), rows = m * kParts;
@@ -404,7 +406,7 @@ struct MoeDownArgs {
   int T, k, lds_bytes;
   const uint16_t* h;
   const MoeEntry* table;
-  float* part;
+  float* part;  // by group of outputs
   const uint8_t* counted;
   uint32_t* arrived;
   char* y;
@@ -412,21 +414,23 @@ struct MoeDownArgs {
 };
 
 // Values that another workgroup of the kernel reads: stores and loads of the
-// device's scope, which pass by the caches that are not coherent between the
-// XCDs.  A wave's stores have reached memory once it has waited for them; then
-// it may be counted as arrived.  (A fence of that scope writes back all of an
-// XCD's L2: 26 us for the kernel of one token, 8 of 64 experts 1408 -> 2048, and 11 so.)
+// device's scope (bit sc1), which pass by the caches that are not coherent
+// between the XCDs.  A wave's stores have reached memory once it has waited for
+// them; then it may be counted as arrived.  (A fence of that scope writes back
+// all of an XCD's L2: 26 us for the kernel of one token, 8 of 64 experts 1408 ->
+// 2048, and 11 so.)
+constexpr int kDeviceScope = 16;
 __device__ __forceinline__ void moe_publish(float* p, float v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ float moe_collect(const float* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
 __device__ __forceinline__ void moe_published() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ f32x4_t moe_collect(rsrc_t r, uint32_t at) {
+  return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, kDeviceScope));
+}
 
 // A wave owns NB blocks of 16 outputs.
 template <typename E, int KIND, int SUB, int NT, int NB, int WK, int U>
-__global__ __launch_bounds__(64 * (kMoeDownBlocks / NB) * WK) __attribute__((amdgpu_waves_per_eu(2)))
+__global__ __launch_bounds__(64 * (kMoeDownBlocks / NB) * WK) __attribute__((amdgpu_waves_per_eu(NT == 1 ? 4 : 2)))
 void moe_down_kernel(const MoeDownArgs p) {
   constexpr int kParts = E::kBytes == 2 ? 2 : 3, W = kMoeDownBlocks / NB * WK;
   constexpr int kTokens = 16 * NT / kParts;
@@ -437,7 +441,9 @@ void moe_down_kernel(const MoeDownArgs p) {
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wb = w / WK, wk = w % WK;
   const MoeEntry& t = p.table[blockIdx.y];
-  const int e = t.e, cnt = t.cnt, o0 = (int)blockIdx.x * kMoeDownBlocks * 16;
+  constexpr int kCols = 16 * kMoeDownBlocks;
+  const int e = t.e, cnt = t.cnt, o0 = (int)blockIdx.x * kCols, R = p.T * p.k;
+  float* part = p.part + (int64_t)blockIdx.x * R * kCols;
   typedef MoeStream<KIND, SUB, (kParts > 2), NB, NT, WK, U> Stream;
   const int my_row = t.row[lane];  // behind cnt: not used
   const float my_w = t.w[lane];
@@ -480,7 +486,7 @@ void moe_down_kernel(const MoeDownArgs p) {
       for (int i = tid; i < kMoeDownBlocks * 16 * m; i += 64 * W) {
         const int c = i & 15, b = (i >> 4) % kMoeDownBlocks, r = (i >> 4) / kMoeDownBlocks, o = o0 + 16 * b + c;
         if (o < p.d_out)
-          moe_publish(p.part + (int64_t)s_row[m0 + r] * p.d_out + o,
+          moe_publish(part + (int)s_row[m0 + r] * kCols + 16 * b + c,
                       s_w[m0 + r] * moe_sum<NB, NT, WK, kParts>(red, b / NB * WK, b % NB, m, r, c));
       }
     }
@@ -492,17 +498,24 @@ void moe_down_kernel(const MoeDownArgs p) {
     last = __hip_atomic_fetch_add(&p.arrived[blockIdx.x], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.y - 1;
   __syncthreads();
   if (!last) return;
-  for (int i = tid; i < p.T * kMoeDownBlocks * 4; i += 64 * W) {
-    const int tok = i / (kMoeDownBlocks * 4), o = o0 + 4 * (i % (kMoeDownBlocks * 4));
+  const rsrc_t pr = make_rsrc(part, (uint32_t)(R * kCols * 4));
+  for (int i = tid; i < p.T * (kCols / 4); i += 64 * W) {
+    const int tok = i / (kCols / 4), at = 4 * (i % (kCols / 4)), o = o0 + at;
     if (o >= p.d_out) continue;
     f32x4_t s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int j = 0; j < p.k; ++j) {
-      const int64_t r = (int64_t)tok * p.k + j;
-      if (p.counted[r]) {
+    constexpr int kAhead = 8;  // choices asked for together
+    for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+      f32x4_t v[kAhead];
+      uint8_t counts[kAhead];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) s[v] += moe_collect(p.part + r * p.d_out + o + v);
+      for (int j = 0; j < kAhead; ++j) {
+        const int r = tok * p.k + min(j0 + j, p.k - 1);
+        counts[j] = p.counted[r];
+        v[j] = moe_collect(pr, (uint32_t)(r * kCols + at) * 4u);
       }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (j0 + j < p.k && counts[j]) s += v[j];
     }
     char* dst = p.y + (int64_t)tok * p.ldy_bytes + (int64_t)o * E::kBytes;
     if constexpr (E::kBytes == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
@@ -547,12 +560,13 @@ hipError_t run_up(const MoeCall& c, hipStream_t stream) {
   a.counted = reinterpret_cast<uint8_t*>(c.ws + c.plan.counted);
   a.arrived = reinterpret_cast<uint32_t*>(c.ws + c.plan.arrived);
   a.groups = moe_down_groups(c.down.d_out);
+  a.entries = c.plan.entries;
   a.lds_bytes = moe_lds_bytes(c.T, XFrag<E>::kParts, NT, a.k_tiles, moe_sum_bytes(WB * WK, 2, NT));
   static DynLdsLimit lim;
   const auto kernel = moe_up_kernel<E, KIND, SUB, NT, WB, WK, U>;
   const hipError_t e = ensure_dynamic_lds(lim, reinterpret_cast<const void*>(kernel), (size_t)a.lds_bytes);
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)((a.h_tiles * 8 + WB - 1) / WB), (unsigned)c.plan.entries);
+  const dim3 grid((unsigned)((a.h_tiles * 8 + WB - 1) / WB), (unsigned)c.plan.entries + 1);
   hipLaunchKernelGGL(kernel, grid, dim3(64 * WB * WK), (size_t)a.lds_bytes, stream, a);
   return hipGetLastError();
 }
