@@ -28,12 +28,13 @@ struct W8GemmArgs {
   int tiles_o, tiles_t;
 };
 
-constexpr int kRows = 256, kCols = 256, kStep = 128;  // of a workgroup; inputs of a stage
+constexpr int kRows = 256, kCols = 256, kStep = 64;  // of a workgroup; inputs of a stage
 constexpr int kWaves = 8;
 constexpr int kRowTiles = 8, kOutTiles = 4;  // 16 x 16 products of a wave
-constexpr int kStageBytes = kRows * kStep;
-constexpr int kLoads = kStageBytes / 1024 / kWaves;  // of a wave and stage
-constexpr int kTileOrder = 4;                        // row tiles walked together
+constexpr int kRowBytes = kRows * kStep, kCodeBytes = kCols * kStep, kStageBytes = kRowBytes + kCodeBytes;
+constexpr int kStages = 4;  // in LDS
+constexpr int kLoads = kRowBytes / 1024 / kWaves;  // of a wave, stage and operand
+constexpr int kTileOrder = 4;                      // row tiles walked together
 
 // Block b -> tile: each XCD (b % 8) takes a run of consecutive tiles, and the
 // order walks groups of kTileOrder row tiles across all output tiles, so that
@@ -53,31 +54,57 @@ __device__ __forceinline__ void dma16(rsrc_t r, char* dst, uint32_t voff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, voff, 0, 0, 0);
 }
 
-// One stage: rows at `rd`, tiles of codes in registers, while the next rows go
-// to `wr`, another buffer, which restrict tells the compiler: no read waits for
-// the loads in flight.
-__device__ __forceinline__ void stage(const char* __restrict__ rd, char* __restrict__ wr, bool more, rsrc_t xr,
-                                      const uint32_t (&src)[kLoads], const uint4 (&b)[2][kOutTiles], uint32_t lane_row,
-                                      int h, int sw, i32x4_t (&acc)[kRowTiles][kOutTiles]) {
-  if (more)
+// The operands of one 64-input step of a wave.
+struct Step {
+  uint4 x[kRowTiles], b[kOutTiles];
+};
+
+// Loads of a stage: rows of x and tiles of codes, 1 KiB each.
+struct Loader {
+  rsrc_t xr, cr;
+  uint32_t row_at[kLoads], code_at[kLoads];
+  uint32_t piece, last_piece, k_tiles, place;
+  __device__ __forceinline__ void fill(char* dst, int st) const {
+    const uint32_t k = min((uint32_t)st * kStep + piece, last_piece);
+    const uint32_t c = (uint32_t)st < k_tiles ? (uint32_t)st * kW8BlockBytes : kOutOfRange;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) dma16(xr, wr + i * 1024 * kWaves, src[i]);
-  __builtin_amdgcn_s_setprio(1);
+    for (int i = 0; i < kLoads; ++i) {
+      dma16(xr, dst + 1024 * kWaves * i + place, row_at[i] + k);
+      dma16(cr, dst + kRowBytes + 1024 * kWaves * i + place, code_at[i] + c);
+    }
+  }
+};
+
+// The products of step `now`, while the operands of the next one are read from
+// `rows` and `codes` and stage `st` is asked for into `dst`, another buffer, which
+// restrict tells the compiler: no read waits for those loads.
+__device__ __forceinline__ void step(const Step& now, Step& next, const char* __restrict__ rows,
+                                     const char* __restrict__ codes, char* __restrict__ dst, const Loader& ld, int st,
+                                     i32x4_t (&acc)[kRowTiles][kOutTiles]) {
+  ld.fill(dst, st);
+#pragma unroll
+  for (int a = 0; a < kOutTiles; ++a) next.b[a] = ld16(codes + a * kW8TileBytes);
+#pragma unroll
+  for (int t = 0; t < kRowTiles; ++t) next.x[t] = ld16(rows + t * 16 * kStep);
 #pragma unroll
   for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 x = ld16(rd + lane_row + t * 16 * kStep + (((4 * j + h) ^ sw) << 4));
+    for (int a = 0; a < kOutTiles; ++a) acc[t][a] = mfma_i8(now.b[a], now.x[t], acc[t][a]);
+  // Issue order: the reads spread between the products.
+  __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
 #pragma unroll
-      for (int a = 0; a < kOutTiles; ++a) acc[t][a] = mfma_i8(b[j][a], x, acc[t][a]);
-    }
-  __builtin_amdgcn_s_setprio(0);
+  for (int i = 0; i < kRowTiles + kOutTiles; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if (i < 2 * kLoads) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, kRowTiles * kOutTiles - 2 * (kRowTiles + kOutTiles + 1), 0);
 }
 
 template <typename E>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void w8_gemm_kernel(const W8GemmArgs p) {
-  __shared__ __align__(16) char lds[2 * kStageBytes];
+  extern __shared__ __align__(16) char lds[];  // kStages stages
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15, h = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w >> 2, wo = w & 3;
   int to, tt;
@@ -85,68 +112,73 @@ void w8_gemm_kernel(const W8GemmArgs p) {
   const int64_t t0 = (int64_t)tt * kRows;
   const int m = min(kRows, (int)(p.T - t0));
 
-  // Tiles of codes of the wave's 64 outputs: two of inputs per stage, past the
-  // last one zeros (out of the buffer's range).
-  const int blocks = (p.d_out + kW8Block - 1) / kW8Block, blk = min(to * (kCols / kW8Block) + wo, blocks - 1);
+  // Codes: 1 KiB loads, tile for tile as they lie in memory.  Load i of wave w is
+  // tile 8 i + w of a stage's 16: [block][tile].  Past the last step zeros
+  // (out of the buffer's range), as past the last block.
+  const int blocks = (p.d_out + kW8Block - 1) / kW8Block;
   const uint32_t block_bytes = (uint32_t)p.k_tiles * kW8BlockBytes;  // at most 2^23
-  const rsrc_t cr = make_rsrc(p.codes + (int64_t)blk * block_bytes, block_bytes);
-  uint4 next[2][kOutTiles];
-  auto fetch = [&](int st) {
+  const int blk0 = to * (kCols / kW8Block);
+  Loader ld;
+  ld.cr = make_rsrc(p.codes + (int64_t)blk0 * block_bytes, (uint32_t)min(kCols / kW8Block, blocks - blk0) * block_bytes);
+  ld.k_tiles = (uint32_t)p.k_tiles;
+  ld.place = 1024 * w;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int a = 0; a < kOutTiles; ++a)
-        next[j][a] = buf_ld16(cr, 16 * lane + a * kW8TileBytes, (uint32_t)(2 * st + j) * kW8BlockBytes);
-  };
+  for (int i = 0; i < kLoads; ++i) ld.code_at[i] = (uint32_t)(2 * i + (w >> 2)) * block_bytes + (w & 3) * kW8TileBytes + 16 * lane;
 
-  // Rows: a wave-wide load fills 1 KiB, eight rows of 128 bytes; slot i of a
-  // row holds piece i ^ (row % 8), so that the rows of one matrix-core read lie
+  // Rows: a wave-wide load fills 1 KiB, 16 rows of 64 bytes; slot i of a row
+  // holds piece i ^ (row / 4 % 4), so that the rows of one matrix-core read lie
   // on all banks.  Rows past m repeat the last, pieces past d_in the last too
   // (their weights are zeros).
-  const rsrc_t xr = make_rsrc(p.q + t0 * p.ldq, (uint32_t)((m - 1) * p.ldq + ((p.d_in + 15) & ~15)));
-  const uint32_t last_piece = (uint32_t)(p.d_in - 1) & ~15u;
-  uint32_t row_at[kLoads];
-  const uint32_t piece = (uint32_t)(((lane & 7) ^ (lane >> 3)) << 4);
+  ld.xr = make_rsrc(p.q + t0 * p.ldq, (uint32_t)((m - 1) * p.ldq + ((p.d_in + 15) & ~15)));
+  ld.last_piece = (uint32_t)(p.d_in - 1) & ~15u;
+  ld.piece = (uint32_t)(((lane & 3) ^ (lane >> 4)) << 4);
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) row_at[i] = (uint32_t)min(8 * (kWaves * i + w) + (lane >> 3), m - 1) * (uint32_t)p.ldq;
-  auto sources = [&](int st, uint32_t (&src)[kLoads]) {
-    const uint32_t k = min((uint32_t)st * kStep + piece, last_piece);
+  for (int i = 0; i < kLoads; ++i) ld.row_at[i] = (uint32_t)min(16 * (kWaves * i + w) + (lane >> 2), m - 1) * (uint32_t)p.ldq;
+  // The rows' scales are asked for first: at the end, one after the other, they
+  // took 3 us of the whole at 8192 rows 4096 -> 14336.
+  float sx[kRowTiles];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) src[i] = row_at[i] + k;
-  };
-  char* fill = lds + 1024 * w;
-  const int stages = (p.k_tiles + 1) / 2;
+  for (int t = 0; t < kRowTiles; ++t) sx[t] = p.s[t0 + min(wr * 128 + 16 * t + col, m - 1)];
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int st = 0; st < kStages; ++st) ld.fill(lds + st * kStageBytes, st);
 
-  uint32_t src[kLoads];
-  fetch(0);
-  sources(0, src);
-#pragma unroll
-  for (int i = 0; i < kLoads; ++i) dma16(xr, fill + i * 1024 * kWaves, src[i]);
   i32x4_t acc[kRowTiles][kOutTiles];
 #pragma unroll
   for (int t = 0; t < kRowTiles; ++t)
 #pragma unroll
     for (int a = 0; a < kOutTiles; ++a) acc[t][a] = i32x4_t{0, 0, 0, 0};
-
-  const uint32_t lane_row = (uint32_t)(wr * 128 + col) * kStep;
-  for (int st = 0; st < stages; ++st) {
-    const bool more = st + 1 < stages;
-    // This stage's rows and codes were asked for a stage ago; every wave has
-    // finished with the buffer that is filled next: its reads of it have ended
-    // (lgkmcnt), which the barrier itself does not wait for.
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  // A lane's places in a stage.
+  const uint32_t rows_at = (uint32_t)(wr * 128 + col) * kStep + (uint32_t)((h ^ (col >> 2)) << 4);
+  const uint32_t codes_at = (uint32_t)(kRowBytes + wo * kW8BlockBytes + 16 * lane);
+  Step s0, s1;
+  // Until at most the loads of kBehind stages are in flight, and every wave's
+  // reads have ended (lgkmcnt), which the barrier itself does not wait for.
+  constexpr int kPer = 2 * kLoads, kBehind = (kStages - 2) * kPer, kFirst = (kStages - 1) * kPer;
+  __builtin_amdgcn_s_waitcnt((kFirst & 15) | ((kFirst >> 4) << 14) | 0x0070);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int a = 0; a < kOutTiles; ++a) s0.b[a] = ld16(lds + codes_at + a * kW8TileBytes);
+#pragma unroll
+  for (int t = 0; t < kRowTiles; ++t) s0.x[t] = ld16(lds + rows_at + t * 16 * kStep);
+  // Stage st: its operands are in registers, those of the next are read; its
+  // buffer takes stage st + kStages.  Past the last stage the same loads are
+  // asked for (the last rows again, zeros for codes), so that what is in flight
+  // is always the same number.
+  auto turn = [&](int st, const Step& now, Step& next) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((kBehind & 15) | ((kBehind >> 4) << 14) | 0x0070);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    uint4 b[2][kOutTiles];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int a = 0; a < kOutTiles; ++a) b[j][a] = next[j][a];
-    fetch(more ? st + 1 : st);
-    sources(st + 1, src);
-    const int cur = st & 1;
-    stage(lds + cur * kStageBytes, fill + (cur ^ 1) * kStageBytes, more, xr, src, b, lane_row, h, col & 7, acc);
+    const char* from = lds + ((st + 1) % kStages) * kStageBytes;
+    step(now, next, from + rows_at, from + codes_at, lds + (st % kStages) * kStageBytes, ld, st + kStages, acc);
+  };
+  for (int st = 0; st < p.k_tiles; st += 2) {  // of an odd number, one step of zeros more
+    turn(st, s0, s1);
+    turn(st + 1, s1, s0);
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may write LDS that is another workgroup's
 
   const int o0 = to * kCols + wo * kW8Block;
   if (o0 >= p.d_out) return;
@@ -160,14 +192,23 @@ void w8_gemm_kernel(const W8GemmArgs p) {
   for (int t = 0; t < kRowTiles; ++t) {
     const int row = wr * 128 + 16 * t + col;
     if (row >= m) continue;
-    const float sx = p.s[t0 + row];
     char* y = p.y + (t0 + row) * p.ldy_bytes;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int o = o0 + 32 * g + 8 * h;
-      if (o < p.d_out) w8_store8<E>(y + (int64_t)o * E::kBytes, acc[t][2 * g], acc[t][2 * g + 1], sx, ws[g][0], ws[g][1]);
+      if (o < p.d_out) w8_store8<E>(y + (int64_t)o * E::kBytes, acc[t][2 * g], acc[t][2 * g + 1], sx[t], ws[g][0], ws[g][1]);
     }
   }
+}
+
+template <typename E>
+hipError_t launch_gemm(const W8GemmArgs& a, hipStream_t stream) {
+  constexpr size_t lds = kStages * kStageBytes;
+  static DynLdsLimit lim;
+  const hipError_t e = ensure_dynamic_lds(lim, reinterpret_cast<const void*>(w8_gemm_kernel<E>), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((w8_gemm_kernel<E>), dim3((unsigned)(a.tiles_o * a.tiles_t)), dim3(64 * kWaves), lds, stream, a);  // at most 2^12 * 2^12
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -187,10 +228,7 @@ hipError_t launch_w8_gemm(const W8Call& c, hipStream_t stream) {
   a.T = c.T;
   a.tiles_o = (c.w.d_out + kCols - 1) / kCols;
   a.tiles_t = (c.T + kRows - 1) / kRows;
-  const unsigned grid = (unsigned)(a.tiles_o * a.tiles_t);  // at most 2^12 * 2^12
-  if (c.dtype == LORA_DTYPE_BF16) hipLaunchKernelGGL((w8_gemm_kernel<BF16>), dim3(grid), dim3(64 * kWaves), 0, stream, a);
-  else hipLaunchKernelGGL((w8_gemm_kernel<F32>), dim3(grid), dim3(64 * kWaves), 0, stream, a);
-  return hipGetLastError();
+  return c.dtype == LORA_DTYPE_BF16 ? launch_gemm<BF16>(a, stream) : launch_gemm<F32>(a, stream);
 }
 
 }  // namespace lora
