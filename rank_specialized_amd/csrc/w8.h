@@ -37,7 +37,7 @@ inline int64_t w8_row_bytes(int d_in) { return ((int64_t)d_in + 15) / 16 * 16; }
 // How a call is run, and the workspace it takes.
 struct W8Plan {
   bool fused;   // few rows: each workgroup rounds them by itself
-  bool many;    // the many-rows kernel
+  int tile;     // rows and outputs per workgroup of the many-rows kernel; 0: the few-rows kernel
   int rt, nt;   // few rows: tiles of 16 outputs and of 16 rows of a workgroup
   size_t q, s;  // rounded rows and their scales
   size_t ws_bytes;
@@ -46,11 +46,34 @@ struct W8Plan {
 constexpr int kW8FusedRows = 4;
 constexpr int kW8FusedValues = 5 * 8 * 512;  // kHold pieces of 8 per thread (w8_rows.hip)
 
+constexpr int kW8BigTile = 256, kW8MidTile = 128, kW8SmallTile = 64;  // small: of the few-rows kernel
+
+// What a kernel with tiles of `tile` rows and outputs takes, in us, up to a
+// constant.  Workgroups run one to a compute unit, so in rounds of 256; one's
+// time goes with its tiles of inputs, and faster the emptier the round.  The
+// constants are fitted to times measured at 48 to 3000 rows of ten shapes from
+// 512 -> 2048 to 18944 -> 3584 (us, small, mid, big): 256 rows 3584 -> 3584 10.6,
+// 16.8, 37.6; 512 rows 19.0, 17.4, 37.8; 1024 rows 34, 18.8, 38.5; 1024 rows 3584
+// -> 14336 151, 72, 51; 2048 rows 286, 124, 95; 200 rows 2048 -> 8192 15.0, 12.1,
+// 24.3; 3000 rows 18944 -> 3584 420, 243, 193.
+inline double w8_many_us(int tile, int T, int d_out, int kt) {
+  const double empty = tile == kW8BigTile ? 0.52 : (tile == kW8MidTile ? 0.17 : 0.055);
+  const double load = tile == kW8BigTile ? 0.27 : (tile == kW8MidTile ? 0.09 : 0.055);
+  const double start = tile == kW8BigTile ? 4.0 : 4.5;
+  const int64_t groups = (int64_t)((T + tile - 1) / tile) * ((d_out + tile - 1) / tile), full = groups / 256, rest = groups % 256;
+  return (double)full * (kt * (empty + load) + start) + (rest > 0 ? kt * (empty + load * (double)rest / 256.) + start : 0.);
+}
+
 inline W8Plan w8_plan_call(int d_in, int d_out, int T, bool quantized) {
   W8Plan p{};
   if (T <= 0) return p;
   const int64_t per_row = ((int64_t)d_in + 511) / 512 * 512;
-  p.many = T > 256;
+  if (T > 32) {
+    const int kt = w8_k_tiles(d_in);
+    const double small = w8_many_us(kW8SmallTile, T, d_out, kt), mid = w8_many_us(kW8MidTile, T, d_out, kt),
+                 big = w8_many_us(kW8BigTile, T, d_out, kt);
+    if (small > mid || small > big) p.tile = mid < big ? kW8MidTile : kW8BigTile;
+  }
   p.nt = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
   // Tiles of outputs per workgroup: more share the rows' loads, fewer give
   // every compute unit work.

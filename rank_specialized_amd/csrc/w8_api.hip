@@ -41,7 +41,7 @@ int check_w8_codes(const int8_t* q, int64_t ldq, int d_in, const float* scales, 
 }
 
 int run_w8(W8Call& c, hipStream_t stream) {
-  const hipError_t e = c.plan.many ? launch_w8_gemm(c, stream) : launch_w8_rows(c, stream);
+  const hipError_t e = c.plan.tile > 0 ? launch_w8_gemm(c, stream) : launch_w8_rows(c, stream);
   return e == hipSuccess ? LORA_OK : hip_fail(e);
 }
 
