@@ -26,7 +26,7 @@ def kernel(T, d_in, d_out):
     nt = 1 if T <= 16 else (2 if T <= 32 else 4)
     tiles = -(-d_out // 64) * 4 * -(-T // (16 * nt))
     rt = 4 if nt == 4 or tiles >= 2048 else (2 if tiles >= 512 else 1)
-    return nt, rt, T <= 4 and T * (-(-d_in // 512) * 512) <= 20480
+    return nt, rt, T <= 16 and T * (-(-d_in // 512) * 512) <= (20480 if T <= 4 else 12288)
 
 
 def test_sizes_reach_every_kernel():
