@@ -73,17 +73,34 @@ inline W8Plan w8_plan_call(int d_in, int d_out, int T, bool quantized) {
   W8Plan p{};
   if (T <= 0) return p;
   const int64_t per_row = ((int64_t)d_in + 511) / 512 * 512;
+  const int blocks = w8_blocks(d_out);
   if (T > 32) {
-    const int kt = w8_k_tiles(d_in);
-    const double small = w8_many_us(kW8SmallTile, T, d_out, kt), mid = w8_many_us(kW8MidTile, T, d_out, kt),
-                 big = w8_many_us(kW8BigTile, T, d_out, kt);
-    if (small > mid || small > big) p.tile = mid < big ? kW8MidTile : kW8BigTile;
+    // The smallest tiles that give every compute unit one workgroup at most; the
+    // largest ones where none do, if the many-rows kernel does not take less.
+    // (rows x outputs, us) 64 rows 3584 -> 512 16 x 32 4.0, 32 x 32 4.4, 32 x 64 5.6,
+    // 64 x 64 7.6; 64 rows 3584 -> 3584 7.3, 6.3, 7.6, 10.6; 128 rows 11.0, 8.7, 7.8,
+    // 10.5; 256 rows 17.1, 14.0, 11.9, 10.8; 48 rows 18944 -> 3584 25.6, 16.7, 22.2, 31.5.
+    p.rt = p.nt = 4;
+    for (const int shape : {21, 22, 42}) {
+      const int rt = shape / 10, nt = shape % 10;
+      if ((int64_t)blocks * (4 / rt) * ((T + 16 * nt - 1) / (16 * nt)) > 256) continue;
+      p.rt = rt;
+      p.nt = nt;
+      break;
+    }
+    if (p.nt == 4) {
+      const int kt = w8_k_tiles(d_in);
+      const double small = w8_many_us(kW8SmallTile, T, d_out, kt), mid = w8_many_us(kW8MidTile, T, d_out, kt),
+                   big = w8_many_us(kW8BigTile, T, d_out, kt);
+      if (small > mid || small > big) p.tile = mid < big ? kW8MidTile : kW8BigTile;
+    }
+  } else {
+    p.nt = T <= 16 ? 1 : 2;
+    // Tiles of outputs per workgroup: more share the rows' loads, fewer give
+    // every compute unit work.
+    const int64_t tiles = (int64_t)blocks * 4;
+    p.rt = tiles < 512 ? 1 : (tiles < 2048 ? 2 : 4);
   }
-  p.nt = T <= 16 ? 1 : (T <= 32 ? 2 : 4);
-  // Tiles of outputs per workgroup: more share the rows' loads, fewer give
-  // every compute unit work.
-  const int64_t tiles = (int64_t)w8_blocks(d_out) * 4 * ((T + 16 * p.nt - 1) / (16 * p.nt));
-  p.rt = p.nt == 4 ? 4 : (tiles < 512 ? 1 : (tiles < 2048 ? 2 : 4));
   p.fused = !quantized && T <= kW8FusedRows && T * per_row <= (T <= 4 ? kW8FusedValues : kW8FusedSome);
   if (!quantized && !p.fused) {
     p.q = p.ws_bytes;

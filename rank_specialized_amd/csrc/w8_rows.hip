@@ -232,18 +232,14 @@ hipError_t launch_rows(const W8RowsArgs& a, const W8Plan& pl, hipStream_t stream
       default: return launch_one<E, 4, 1, 2, 8, true>(a, stream);
     }
   }
-  if (pl.nt == 4) return launch_one<E, 4, 4, 2, 8, false>(a, stream);
-  if (pl.nt == 2) {
-    switch (pl.rt) {
-      case 1: return launch_one<E, 1, 2, 4, 8, false>(a, stream);
-      case 2: return launch_one<E, 2, 2, 2, 8, false>(a, stream);
-      default: return launch_one<E, 4, 2, 2, 8, false>(a, stream);
-    }
-  }
-  switch (pl.rt) {
-    case 1: return launch_one<E, 1, 1, 4, 8, false>(a, stream);
-    case 2: return launch_one<E, 2, 1, 4, 8, false>(a, stream);
-    default: return launch_one<E, 4, 1, 2, 8, false>(a, stream);
+  switch (10 * pl.rt + pl.nt) {
+    case 11: return launch_one<E, 1, 1, 4, 8, false>(a, stream);
+    case 21: return launch_one<E, 2, 1, 4, 8, false>(a, stream);
+    case 41: return launch_one<E, 4, 1, 2, 8, false>(a, stream);
+    case 12: return launch_one<E, 1, 2, 4, 8, false>(a, stream);
+    case 22: return launch_one<E, 2, 2, 2, 8, false>(a, stream);
+    case 42: return launch_one<E, 4, 2, 2, 8, false>(a, stream);
+    default: return launch_one<E, 4, 4, 2, 8, false>(a, stream);
   }
 }
 

@@ -19,14 +19,15 @@ def kernel(T, d_in, d_out):
     """The tile of the many-rows kernel, or (tiles of rows, tiles of outputs,
     rounded in the kernel) of the few-rows kernel."""
     kt = -(-d_in // 64)
+    blocks = -(-d_out // 64)
     if T > 32:
+        for rt, nt in ((2, 1), (2, 2), (4, 2)):
+            if blocks * (4 // rt) * -(-T // (16 * nt)) <= 256:
+                return nt, rt, False
         small, mid, big = (us(t, T, d_out, kt) for t in (64, 128, 256))
-        if small > mid or small > big:
-            return 128 if mid < big else 256
-    nt = 1 if T <= 16 else (2 if T <= 32 else 4)
-    tiles = -(-d_out // 64) * 4 * -(-T // (16 * nt))
-    rt = 4 if nt == 4 or tiles >= 2048 else (2 if tiles >= 512 else 1)
-    return nt, rt, T <= 16 and T * (-(-d_in // 512) * 512) <= (20480 if T <= 4 else 12288)
+        return (4, 4, False) if small <= mid and small <= big else (128 if mid < big else 256)
+    rt = 4 if blocks >= 512 else (2 if blocks >= 128 else 1)
+    return 1 if T <= 16 else 2, rt, T <= 16 and T * (-(-d_in // 512) * 512) <= (20480 if T <= 4 else 12288)
 
 
 def test_sizes_reach_every_kernel():
