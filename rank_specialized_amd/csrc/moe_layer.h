@@ -4,7 +4,7 @@
 //   y[t]    = sum_j w[t, j] D_e h[t, e]
 //
 // with 4-bit matrices (w4.h).  What bounds both is the stream of codes.  In
-// both, a workgroup owns 16 WB outputs of one expert for the tokens that chose
+// both, a workgroup owns some blocks of 16 outputs of one expert for the tokens that chose
 // it: the rows lie in LDS, WK waves share the 128-input tiles of 16 outputs,
 // and their sums meet in LDS, in wave order.  Codes enter the bf16 matrix cores
 // as in the few-rows products (w4_rows.h): 32 + q with (32 + z) times the rows'
@@ -430,9 +430,9 @@ __device__ __forceinline__ f32x4_t moe_collect(rsrc_t r, uint32_t at) {
 
 // A wave owns NB blocks of 16 outputs.
 template <typename E, int KIND, int SUB, int NT, int NB, int WK, int U>
-__global__ __launch_bounds__(64 * (kMoeDownBlocks / NB) * WK) __attribute__((amdgpu_waves_per_eu(NT == 1 ? 4 : 2)))
+__global__ __launch_bounds__(64 * (moe_down_blocks(NT == 2) / NB) * WK) __attribute__((amdgpu_waves_per_eu(NT == 1 ? 4 : 2)))
 void moe_down_kernel(const MoeDownArgs p) {
-  constexpr int kParts = E::kBytes == 2 ? 2 : 3, W = kMoeDownBlocks / NB * WK;
+  constexpr int kParts = E::kBytes == 2 ? 2 : 3, kBlocks = moe_down_blocks(NT == 2), W = kBlocks / NB * WK;
   constexpr int kTokens = 16 * NT / kParts;
   extern __shared__ __align__(16) char lds[];
   __shared__ uint16_t s_row[LORA_W4_MOE_MAX_TOKENS];
@@ -441,7 +441,7 @@ void moe_down_kernel(const MoeDownArgs p) {
   const int tid = (int)threadIdx.x, lane = tid & 63, col = lane & 15;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wb = w / WK, wk = w % WK;
   const MoeEntry& t = p.table[blockIdx.y];
-  constexpr int kCols = 16 * kMoeDownBlocks;
+  constexpr int kCols = 16 * kBlocks;
   const int e = t.e, cnt = t.cnt, o0 = (int)blockIdx.x * kCols, R = p.T * p.k;
   float* part = p.part + (int64_t)blockIdx.x * R * kCols;
   typedef MoeStream<KIND, SUB, (kParts > 2), NB, NT, WK, U> Stream;
@@ -451,7 +451,7 @@ void moe_down_kernel(const MoeDownArgs p) {
     Stream st;
 #pragma unroll
     for (int a = 0; a < NB; ++a) {
-      const int64_t tile0 = (int64_t)min((int)blockIdx.x * kMoeDownBlocks + wb * NB + a, p.row_tiles - 1) * p.k_tiles;
+      const int64_t tile0 = (int64_t)min((int)blockIdx.x * kBlocks + wb * NB + a, p.row_tiles - 1) * p.k_tiles;
       st.code0[a] = p.codes + e * p.code_stride + tile0 * kW4TileBytes;
       st.par0[a] = p.params + e * p.param_stride + tile0 * kW4Rows * Stream::Par::kBytes;
     }
@@ -483,8 +483,8 @@ void moe_down_kernel(const MoeDownArgs p) {
           },
           [&](int, int) {});
       const float* red = reinterpret_cast<const float*>(lds);
-      for (int i = tid; i < kMoeDownBlocks * 16 * m; i += 64 * W) {
-        const int c = i & 15, b = (i >> 4) % kMoeDownBlocks, r = (i >> 4) / kMoeDownBlocks, o = o0 + 16 * b + c;
+      for (int i = tid; i < kBlocks * 16 * m; i += 64 * W) {
+        const int c = i & 15, b = (i >> 4) % kBlocks, r = (i >> 4) / kBlocks, o = o0 + 16 * b + c;
         if (o < p.d_out)
           moe_publish(part + (int)s_row[m0 + r] * kCols + 16 * b + c,
                       s_w[m0 + r] * moe_sum<NB, NT, WK, kParts>(red, b / NB * WK, b % NB, m, r, c));
@@ -559,7 +559,7 @@ hipError_t run_up(const MoeCall& c, hipStream_t stream) {
   a.table = reinterpret_cast<MoeEntry*>(c.ws + c.plan.table);
   a.counted = reinterpret_cast<uint8_t*>(c.ws + c.plan.counted);
   a.arrived = reinterpret_cast<uint32_t*>(c.ws + c.plan.arrived);
-  a.groups = moe_down_groups(c.down.d_out);
+  a.groups = c.plan.down_groups;
   a.entries = c.plan.entries;
   a.lds_bytes = moe_lds_bytes(c.T, XFrag<E>::kParts, NT, a.k_tiles, moe_sum_bytes(WB * WK, 2, NT));
   static DynLdsLimit lim;
@@ -590,31 +590,48 @@ hipError_t run_down(const MoeCall& c, hipStream_t stream) {
   a.arrived = reinterpret_cast<uint32_t*>(c.ws + c.plan.arrived);
   a.y = reinterpret_cast<char*>(c.y);
   a.ldy_bytes = c.ldy * E::kBytes;
-  a.lds_bytes = moe_lds_bytes(c.T, moe_h_parts(c.dtype), NT, a.k_tiles, moe_sum_bytes(kMoeDownBlocks / NB * WK, NB, NT));
+  constexpr int kWaves = moe_down_blocks(NT == 2) / NB * WK;
+  a.lds_bytes = moe_lds_bytes(c.T, moe_h_parts(c.dtype), NT, a.k_tiles, moe_sum_bytes(kWaves, NB, NT));
   static DynLdsLimit lim;
   const auto kernel = moe_down_kernel<E, KIND, SUB, NT, NB, WK, U>;
   const hipError_t e = ensure_dynamic_lds(lim, reinterpret_cast<const void*>(kernel), (size_t)a.lds_bytes);
   if (e != hipSuccess) return e;
-  const dim3 grid((unsigned)moe_down_groups(a.d_out), (unsigned)c.plan.entries);
-  hipLaunchKernelGGL(kernel, grid, dim3(64 * kMoeDownBlocks / NB * WK), (size_t)a.lds_bytes, stream, a);
+  const dim3 grid((unsigned)c.plan.down_groups, (unsigned)c.plan.entries);
+  hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), (size_t)a.lds_bytes, stream, a);
   return hipGetLastError();
 }
 
-// Two 16-row tiles where an expert has more tokens, on average, than about half
-// of what one holds.
-inline bool moe_two_tiles(const MoeCall& c, int parts) {
-  return c.T > 16 / parts && 2 * c.T * c.k * parts > 16 * c.gate.n;
-}
-
+// Waves to a block of 16 outputs, and blocks to a workgroup.
+// Kernel 1: two waves share a block's inputs, four blocks to a
+// workgroup.  Two departures:
+// - float32 rows whose workgroups would not reach every compute unit: one block,
+//   four waves.  These kernels are bound by the instructions that widen codes,
+//   so a unit without work counts (3 tokens, 6 of 8 experts 4096 -> 1368: kernel
+//   1 20.3 us, and 23.3 with the four blocks).
+// - wide layers of four tokens or more an expert, a group to a tile: a wave to
+//   all inputs of a block, eight blocks, so that half as many workgroups bring
+//   the rows (64 tokens, 8 of 64 experts 2048 -> 1408: kernel 1 40.1 us, and
+//   45.1 otherwise; with one token an expert 57 otherwise, and 69 so; with
+//   groups of 32, whose registers do not suffice, 53 otherwise and 74 so).
 template <typename E, int KIND, int SUB>
 hipError_t launch_up(const MoeCall& c, hipStream_t stream) {
-  if (moe_two_tiles(c, XFrag<E>::kParts)) return run_up<E, KIND, SUB, 2, 2, 4, 2>(c, stream);
-  return run_up<E, KIND, SUB, 1, 2, 4, 2>(c, stream);
+  if (c.plan.up_two) return run_up<E, KIND, SUB, 2, 2, 4, 2>(c, stream);
+  if constexpr (XFrag<E>::kParts > 1) {
+    if (2 * c.plan.entries * c.plan.h_tiles < 256) return run_up<E, KIND, SUB, 1, 1, 4, 2>(c, stream);
+  } else if constexpr (SUB == 1) {
+    if (c.plan.up_wide) return run_up<E, KIND, SUB, 1, 8, 1, 3>(c, stream);
+  }
+  return run_up<E, KIND, SUB, 1, 4, 2, 2>(c, stream);
 }
+// Kernel 2: four blocks of their own waves, two to a block (one token, 8 of 64
+// experts 1408 -> 2048: 7.4 us, and 8.9 with eight blocks, two to a wave; 7
+// tokens, 4 of 32: 13.3 and 14.9).  Two 16-row tiles: eight blocks, two to a
+// wave (64 tokens, 8 of 64: 36.2 us, and 42.7 with four blocks): half as many
+// workgroups bring the rows.
 template <typename E, int KIND, int SUB>
 hipError_t launch_down(const MoeCall& c, hipStream_t stream) {
-  if (moe_two_tiles(c, moe_h_parts(c.dtype))) return run_down<E, KIND, SUB, 2, 2, 2, 2>(c, stream);
-  return run_down<E, KIND, SUB, 1, 2, 2, 2>(c, stream);
+  if (c.plan.down_two) return run_down<E, KIND, SUB, 2, 2, 2, 2>(c, stream);
+  return run_down<E, KIND, SUB, 1, 1, 2, 2>(c, stream);
 }
 
 template <typename E, bool UP>
