@@ -972,11 +972,16 @@ def _codes(q: torch.Tensor, T: int, d_in: int, name: str) -> int:
     multiple of 16 values behind the last."""
     if q.dtype != torch.int8 or q.shape != (T, d_in):
         raise ValueError(f"{name} must be int8 [{T}, {d_in}]")
-    ld = _ld(q, name) if T > 1 else (d_in + 15) // 16 * 16
-    if T > 0 and d_in > 1 and q.stride(1) != 1:
+    if T > _INT_MAX or d_in > _INT_MAX:
+        raise ValueError(f"{name} has more rows or columns than an int counts")
+    ld, step = q.stride()
+    if T > 0 and d_in > 1 and step != 1:
         raise ValueError(f"{name} must be 2-D with unit column stride")
-    if T > 0 and d_in % 16 != 0:
-        end = q.storage_offset() + (T - 1) * ld + (d_in + 15) // 16 * 16
+    row = (d_in + 15) // 16 * 16
+    if T <= 1:
+        ld = row
+    if T > 0 and row != d_in:
+        end = q.storage_offset() + (T - 1) * ld + row
         if end > q.untyped_storage().nbytes():
             raise ValueError(f"{name}'s last row must reach to a multiple of 16 values in memory")
     return ld
@@ -993,12 +998,15 @@ def lora_w8_quantize(x: torch.Tensor, q: Optional[torch.Tensor] = None, scales: 
     if index < 0:
         _same_device(index)
     if q is None:
-        q = torch.empty(T, (d_in + 15) // 16 * 16, dtype=torch.int8, device=x.device)[:, :d_in]
+        ldq = (d_in + 15) // 16 * 16
+        q = x.new_empty((T, ldq), dtype=torch.int8)
+        if ldq != d_in:
+            q = q[:, :d_in]
     else:
         _same_device(index, q=q)
-    ldq = _codes(q, T, d_in, "q")
+        ldq = _codes(q, T, d_in, "q")
     if scales is None:
-        scales = torch.empty(T, dtype=torch.float32, device=x.device)
+        scales = x.new_empty((T,), dtype=torch.float32)
     elif scales.shape != (T,) or scales.dtype != torch.float32 or not scales.is_contiguous():
         raise ValueError("scales must be a contiguous float32 [T]")
     else:
@@ -1012,17 +1020,17 @@ def lora_w8_workspace_bytes(store: W8Store, T: int, quantized: bool = False) -> 
     return int(L.lib().lora_w8_workspace_bytes(store.ref(), _int(T, "T"), int(quantized)))
 
 
-def _w8_out(store: W8Store, T: int, y, dtype: torch.dtype, device):
+def _w8_out(store: W8Store, T: int, y, dtype: torch.dtype, like: torch.Tensor):
     """y, and its row stride."""
     if y is None:
-        return torch.empty(T, store.d_out, dtype=dtype, device=device), store.d_out
+        return like.new_empty((T, store.d_out), dtype=dtype), store.d_out
     if y.shape != (T, store.d_out) or y.dtype != dtype:
         raise ValueError(f"y must be [{T}, {store.d_out}] of {dtype}")
     _same_device(store.device_index, y=y)
     return y, _ld(y, "y")
 
 
-def _w8_ws(store: W8Store, T: int, quantized: bool, ws, device):
+def _w8_ws(store: W8Store, T: int, quantized: bool, ws, like: torch.Tensor):
     """(the workspace tensor, to be held until the call; its pointer; its bytes)"""
     if ws is not None:
         _same_device(store.device_index, ws=ws)
@@ -1035,7 +1043,7 @@ def _w8_ws(store: W8Store, T: int, quantized: bool, ws, device):
         nb = store._ws_bytes[key] = lora_w8_workspace_bytes(store, T, quantized)
     if nb == 0:
         return None, None, 0
-    ws = torch.empty(nb, dtype=torch.uint8, device=device)
+    ws = like.new_empty((nb,), dtype=torch.uint8)
     return ws, ws.data_ptr(), nb
 
 
@@ -1049,8 +1057,8 @@ def lora_w8_apply(store: W8Store, x: torch.Tensor, y: Optional[torch.Tensor] = N
         raise ValueError("x must have d_in columns")
     if x.get_device() != index:
         _same_device(index, x=x)
-    y, ldy = _w8_out(store, T, y, x.dtype, x.device)
-    ws, ws_ptr, nb = _w8_ws(store, T, False, ws, x.device)
+    y, ldy = _w8_out(store, T, y, x.dtype, x)
+    ws, ws_ptr, nb = _w8_ws(store, T, False, ws, x)
     _call("lora_w8_apply", index, store._ref, dt, _p(x), ldx, _p(y), ldy, T, ws_ptr, nb)
     return y
 
@@ -1072,7 +1080,7 @@ def lora_w8_apply_quantized(store: W8Store, q: torch.Tensor, scales: torch.Tenso
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise ValueError("y must be bfloat16 or float32")
-    y, ldy = _w8_out(store, T, y, dtype, q.device)
-    ws, ws_ptr, nb = _w8_ws(store, T, True, ws, q.device)
+    y, ldy = _w8_out(store, T, y, dtype, q)
+    ws, ws_ptr, nb = _w8_ws(store, T, True, ws, q)
     _call("lora_w8_apply_quantized", index, store._ref, _p(q), ldq, _p(scales), dt, _p(y), ldy, T, ws_ptr, nb)
     return y

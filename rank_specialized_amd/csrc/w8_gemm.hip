@@ -2,12 +2,18 @@
 //
 //   y[t, o] = s_x[t] s_w[o] sum_k q_x[t, k] q_w[o, k]
 //
-// bounded by the integer matrix cores and what feeds them.  A workgroup takes
-// 256 rows x 256 outputs, its eight waves 128 rows x 64 outputs each (2 x 4).
-// The rows' codes are staged 128 inputs at a time in LDS, two buffers, by loads
-// that write LDS directly; the weights' tiles are matrix-core operands as they
-// lie in memory, and go straight to registers, one stage ahead: they take no
-// LDS bandwidth, of which the rows alone take most.
+// bounded by the integer matrix cores and, for many rows, by the power that they
+// may take: at 8192 rows 4096 -> 14336 they are busy 85 % of the cycles, and the
+// clock falls to 1.3 to 1.55 GHz (406 us, 2370 TOPS; a large plain product, 8192
+// cubed, reaches 2440).  A workgroup takes 256 rows x 256 outputs, its eight waves
+// 128 x 64 each; or 128 x 128, with two groups of waves over the inputs, where
+// that gives more compute units work (1024 rows 3584 -> 3584 18.8 us, and 38.5
+// with the large ones; the choice is w8_plan_call's).
+//
+// Both operands go through LDS, 64 inputs at a time, in four stages that loads
+// write directly; the operands of a step are read into registers during the
+// products of the one before.  (Weights straight from memory to registers, which
+// their layout allows, with rows staged 128 inputs at a time: 469 us, and 411.)
 #include "host_util.h"
 #include "w8_kernels.h"
 #include "w8_ops.h"

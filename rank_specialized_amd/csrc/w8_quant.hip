@@ -73,8 +73,8 @@ __global__ __launch_bounds__(256) void w8_pack_kernel(int d_in, int d_out, int k
                                                       const void* __restrict__ scales, int scale_dtype,
                                                       char* __restrict__ codes, float* __restrict__ out_scales) {
   const int lane = (int)threadIdx.x & 63, b = (int)threadIdx.x >> 6;
-  const int kt = (int)(blockIdx.x % (unsigned)k_tiles);
-  const int64_t blk = blockIdx.x / (unsigned)k_tiles;
+  const int kt = (int)blockIdx.x;
+  const int64_t blk = blockIdx.y;
   const int64_t o = blk * kW8Block + w8_output(b, lane & 15);
   const int k = kt * kW8K + 16 * (lane >> 4);
   uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void w8_pack_kernel(int d_in, int d_out, int k
       v.z = a.x; v.w = a.y;
     }
   }
-  st16(codes + (int64_t)blockIdx.x * kW8BlockBytes + b * kW8TileBytes + 16 * lane, v);
+  st16(codes + (blk * k_tiles + kt) * kW8BlockBytes + b * kW8TileBytes + 16 * lane, v);
   if (kt == 0 && b == 0) {
     const int64_t c = blk * kW8Block + lane;
     float s = 0.f;
@@ -110,8 +110,8 @@ hipError_t launch_w8_quantize(int dtype, const void* x, int64_t ldx, int T, int 
 
 hipError_t launch_w8_pack(int d_in, int d_out, const int8_t* q, const void* scales, int scale_dtype, void* codes,
                           float* out_scales, hipStream_t stream) {
-  const int64_t grid = (int64_t)w8_blocks(d_out) * w8_k_tiles(d_in);  // at most 2^14 * 2^11
-  hipLaunchKernelGGL(w8_pack_kernel, dim3((unsigned)grid), dim3(256), 0, stream, d_in, d_out, w8_k_tiles(d_in), q, scales,
+  const dim3 grid((unsigned)w8_k_tiles(d_in), (unsigned)w8_blocks(d_out));  // at most 2^11 by 2^14
+  hipLaunchKernelGGL(w8_pack_kernel, grid, dim3(256), 0, stream, d_in, d_out, w8_k_tiles(d_in), q, scales,
                      scale_dtype, reinterpret_cast<char*>(codes), out_scales);
   return hipGetLastError();
 }

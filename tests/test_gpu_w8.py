@@ -227,6 +227,30 @@ def test_bf16_scales_and_a_store_of_rounded_weights():
     same(rs.lora_w8_apply(st, up(x, "bf16", dev)), want_of(x, w8_quantize_ref(W)[0], sb.float().cpu().numpy(), "bf16"))
 
 
+def hbits_t(t):
+    return t.contiguous().view(torch.int16)
+
+
+def test_offsets_past_31_bits():
+    """The last rows of a call with 2^31 bytes of codes of x, and the last
+    outputs of a store of as many, are those of small calls."""
+    dev = device()
+    g = torch.Generator(device=dev).manual_seed(11)
+    d_in, T = 4096, (1 << 19) + 300
+    w = rs.lora_w8_pack(torch.randint(-127, 128, (264, d_in), dtype=torch.int8, device=dev, generator=g), torch.rand(264, device=dev, generator=g))
+    x = torch.empty(T, d_in, dtype=torch.bfloat16, device=dev).normal_(generator=g)
+    y = rs.lora_w8_apply(w, x)
+    assert torch.equal(hbits_t(y[-300:]), hbits_t(rs.lora_w8_apply(w, x[-300:])))
+    assert torch.equal(hbits_t(y[-9:]), hbits_t(rs.lora_w8_apply(w, x[-9:])))
+    del x, y
+    d_in, d_out = 65536, 32768 + 200
+    q, s = torch.randint(-127, 128, (d_out, d_in), dtype=torch.int8, device=dev, generator=g), torch.rand(d_out, device=dev, generator=g)
+    whole, last = rs.lora_w8_pack(q, s), rs.lora_w8_pack(q[-200:], s[-200:])
+    for rows in (1, 9, 300):
+        x = torch.empty(rows, d_in, dtype=torch.bfloat16, device=dev).normal_(generator=g)
+        assert torch.equal(hbits_t(rs.lora_w8_apply(whole, x)[:, -200:]), hbits_t(rs.lora_w8_apply(last, x)))
+
+
 def test_no_rows():
     dev = device()
     st = pack(*weights(12, 24, 40), dev)
