@@ -16,6 +16,14 @@ The 4-bit base layers and the router of a mixture of experts:
     y     = lora_w4_apply(base, x)                            # y = W x; then lora_apply_batched(store, x, y, ...)
     ids, w = lora_route(logits, k)                            # a token's experts and their weights
     y     = lora_w4_apply_experts(experts, x, ids, w)         # y[t] = sum_j w[t, j] W_{ids[t, j]} x
+    y     = lora_w4_moe(gate, up, down, x, ids, w)            # the whole layer of a few tokens
+
+The 8-bit base layers:
+
+    base  = lora_w8_pack(q, scales)                           # int8 codes, a scale per output
+    y     = lora_w8_apply(base, x)                            # x rounded to 8 bits per token on the way
+    qx, sx = lora_w8_quantize(x)                              # once for several layers of one input
+    y     = lora_w8_apply_quantized(base, qx, sx)
 
 Workspaces (lora_workspace_bytes) are allocated here with torch when the
 caller passes none.
