@@ -42,14 +42,13 @@ struct W8Plan {
   size_t q, s;  // rounded rows and their scales
   size_t ws_bytes;
 };
-// Values that a workgroup of the few-rows kernel rounds by itself, at most, and
-// from five rows on, where a kernel for the rows alone costs less than more would.
-// Rounded so, and by a kernel before (us): 8 rows 1024 -> 8192 5.4, 6.5; 12 rows
-// 6.1, 6.6; 8 rows 1280 -> 4096 5.9, 5.9; 5 rows 3584 -> 3584 8.0, 7.8; 12 rows
-// 2048 -> 2048 7.2, 6.2.
+// Rows and values that a workgroup of the few-rows kernel rounds by itself, at
+// most.  Rounded so, and by a kernel before (us, a call in a graph; on its own,
+// where the host's second launch counts): 5 rows 4096 -> 4096 9.5, 9.7; 9.0, 11.1;
+// 5 rows 3584 -> 3584 8.1, 7.9; 7.7, 11.0; 8 rows 2048 -> 2048 6.4, 6.2; 7.0, 11.0;
+// 12 rows 1280 -> 4096 6.8, 5.9; 6.9, 11.0; 8 rows 512 -> 512 4.2, 5.4; 7.2, 11.1.
 constexpr int kW8FusedRows = 16;
 constexpr int kW8FusedValues = 5 * 8 * 512;  // kHold pieces of 8 per thread (w8_rows.hip)
-constexpr int kW8FusedSome = 3 * 8 * 512;
 
 constexpr int kW8BigTile = 256, kW8MidTile = 128, kW8SmallTile = 64;  // small: of the few-rows kernel
 
@@ -101,7 +100,7 @@ inline W8Plan w8_plan_call(int d_in, int d_out, int T, bool quantized) {
     const int64_t tiles = (int64_t)blocks * 4;
     p.rt = tiles < 512 ? 1 : (tiles < 2048 ? 2 : 4);
   }
-  p.fused = !quantized && T <= kW8FusedRows && T * per_row <= (T <= 4 ? kW8FusedValues : kW8FusedSome);
+  p.fused = !quantized && T <= kW8FusedRows && T * per_row <= kW8FusedValues;
   if (!quantized && !p.fused) {
     p.q = p.ws_bytes;
     p.ws_bytes += align_up((size_t)T * (size_t)w8_row_bytes(d_in), 256);

@@ -126,7 +126,7 @@ def test_quantize_outputs_and_neighbours():
 SIZES = [
     (1, 8, 8), (1, 64, 64), (1, 72, 40), (1, 3584, 512), (1, 20480, 72), (1, 20488, 24), (1, 1032, 12296), (1, 264, 40008),
     (2, 1000, 136), (3, 2056, 4104), (4, 512, 264), (4, 5120, 64), (4, 5128, 64), (5, 136, 520), (8, 1000, 136), (16, 520, 72), (12, 1032, 8264), (11, 1024, 33000), (13, 4104, 72),
-    (16, 648, 8200), (16, 1000, 33000), (17, 1032, 200), (30, 3000, 8264), (32, 520, 33000), (33, 776, 136), (64, 2056, 328), (40, 264, 4104), (256, 264, 3592), (200, 520, 3592), (90, 520, 4104), (120, 200, 8200), (70, 72, 1096), (200, 1152, 520),
+    (16, 648, 8200), (16, 1000, 33000), (16, 1544, 33000), (17, 1032, 200), (30, 3000, 8264), (32, 520, 33000), (33, 776, 136), (64, 2056, 328), (40, 264, 4104), (256, 264, 3592), (200, 520, 3592), (90, 520, 4104), (120, 200, 8200), (70, 72, 1096), (200, 1152, 520),
     (256, 136, 264), (256, 200, 14344), (257, 64, 64), (600, 72, 7176), (700, 264, 16392), (300, 200, 328), (513, 1000, 264), (700, 2056, 72), (1030, 128, 1032),
 ]
 

@@ -27,7 +27,7 @@ def kernel(T, d_in, d_out):
         small, mid, big = (us(t, T, d_out, kt) for t in (64, 128, 256))
         return (4, 4, False) if small <= mid and small <= big else (128 if mid < big else 256)
     rt = 4 if blocks >= 512 else (2 if blocks >= 128 else 1)
-    return 1 if T <= 16 else 2, rt, T <= 16 and T * (-(-d_in // 512) * 512) <= (20480 if T <= 4 else 12288)
+    return 1 if T <= 16 else 2, rt, T <= 16 and T * (-(-d_in // 512) * 512) <= 20480
 
 
 def test_sizes_reach_every_kernel():
