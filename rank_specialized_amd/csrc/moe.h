@@ -33,6 +33,7 @@ struct MoePlan {
   size_t h, table;   // h [T k][parts][h_tiles * 128] bf16
   bool up_wide;      // many workgroups of several tokens each, at eight blocks of 16 features
   bool up_two, down_two;  // 16-row tiles of a product
+  bool down_deep;    // few workgroups of long inputs: more waves to a block
   int down_groups;   // of moe_down_blocks blocks
   size_t part;       // [down_groups][T k][16 moe_down_blocks] float32: the choices' weighted outputs
   size_t counted;    // [T k] bytes: whether a choice has such a row
@@ -52,6 +53,7 @@ inline MoePlan moe_plan_call(int n, int ffn, int d_out, int dtype, int T, int k)
   p.down_two = moe_two_tiles(T, k, n, moe_h_parts(dtype));
   const int blocks = moe_down_blocks(p.down_two);
   p.down_groups = (w4_row_tiles(d_out) + blocks - 1) / blocks;
+  p.down_deep = p.entries * p.down_groups <= 256 && p.h_tiles >= 16;
   auto take = [&](size_t bytes) {
     const size_t at = p.ws_bytes;
     p.ws_bytes += align_up(bytes, 256);

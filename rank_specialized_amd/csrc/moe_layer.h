@@ -627,10 +627,14 @@ hipError_t launch_up(const MoeCall& c, hipStream_t stream) {
 // experts 1408 -> 2048: 7.4 us, and 8.9 with eight blocks, two to a wave; 7
 // tokens, 4 of 32: 13.3 and 14.9).  Two 16-row tiles: eight blocks, two to a
 // wave (64 tokens, 8 of 64: 36.2 us, and 42.7 with four blocks): half as many
-// workgroups bring the rows.
+// workgroups bring the rows.  One workgroup at most to a compute unit, and long
+// inputs: eight waves to two blocks (one token, 2 of 8 experts 14336 -> 4096: 19.9
+// us, and 29.4 with two waves to a block; 2 of 16 10752 -> 6144 17.9, 24.4; 2 of 8
+// 4096 -> 4096 8.8, 9.6; with 6 tiles of inputs, 4 of 32 768 -> 2048, 6.3 and 5.8).
 template <typename E, int KIND, int SUB>
 hipError_t launch_down(const MoeCall& c, hipStream_t stream) {
   if (c.plan.down_two) return run_down<E, KIND, SUB, 2, 2, 2, 2>(c, stream);
+  if (c.plan.down_deep) return run_down<E, KIND, SUB, 1, 2, 8, 2>(c, stream);
   return run_down<E, KIND, SUB, 1, 1, 2, 2>(c, stream);
 }
 

@@ -88,11 +88,14 @@ CASES = [
     (64, 8, 64, 64, 40, 64, False, "bf16", "bf16", "silu"),
     (64, 32, 33, 40, 24, 32, True, "bf16", "bf16", "silu"),
     (33, 8, 64, 136, 1032, 128, True, "bf16", "bf16", "silu"),
+    (2, 2, 5, 136, 2056, 32, True, "f32", "bf16", "silu"),
+    (1, 1, 3, 72, 2048, 128, False, "bf16", "bf16", "gelu_tanh"),
     (1, 1, 1, 8, 8, 32, True, "f32", "f32", "gelu_tanh"),
     (1, 4, 8, 520, 136, 64, False, "f32", "f32", "silu"),
     (3, 2, 8, 1032, 344, 64, False, "f32", "f32", "gelu_tanh"),
     (12, 3, 4, 264, 72, 32, True, "bf16", "f32", "silu"),
     (16, 2, 32, 136, 520, 128, False, "f32", "f32", "silu"),
+    (3, 1, 4, 72, 2000, 64, True, "bf16", "f32", "silu"),
     (40, 2, 3, 136, 200, 128, True, "bf16", "f32", "silu"),
 ]
 

@@ -15,11 +15,15 @@ def two_tiles(T, k, n, parts):
 
 def kernels(case):
     """(rows' parts, tiles of 16 rows, blocks, waves to a block) of the first
-    kernel, (tiles of 16 rows, blocks) of the second."""
-    T, k, n, _, ffn, group, _, _, dtype, _ = case
+    kernel, (tiles of 16 rows, blocks, waves to a wave's blocks) of the second."""
+    T, k, n, d, ffn, group, _, _, dtype, _ = case
     x_parts, h_parts = (1, 2) if dtype == "bf16" else (3, 3)
     entries, h_tiles = min(T * k, n), -(-ffn // 128)
-    down = (2, 8) if two_tiles(T, k, n, h_parts) else (1, 4)
+    if two_tiles(T, k, n, h_parts):
+        down = (2, 8, 2)
+    else:
+        deep = entries * -(-d // 64) <= 256 and h_tiles >= 16
+        down = (1, 4, 8 if deep else 2)
     if two_tiles(T, k, n, x_parts):
         return (x_parts, 2, 2, 4), down
     if dtype == "f32" and 2 * entries * h_tiles < 256:
@@ -32,7 +36,7 @@ def kernels(case):
 def test_sizes_reach_every_kernel():
     up, down = zip(*(kernels(c) for c in CASES))
     assert set(up) == {(1, 1, 4, 2), (1, 1, 8, 1), (1, 2, 2, 4), (3, 1, 1, 4), (3, 1, 4, 2), (3, 2, 2, 4)}
-    assert set(zip((u[0] for u in up), down)) == {(p, d) for p in (1, 3) for d in ((1, 4), (2, 8))}
+    assert set(zip((u[0] for u in up), down)) == {(p, d) for p in (1, 3) for d in ((1, 4, 2), (1, 4, 8), (2, 8, 2))}
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(map(str, c)))
