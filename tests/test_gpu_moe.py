@@ -315,3 +315,36 @@ def test_a_block_of_a_decode_step(T):
     ri, rw = route_ref(logits.cpu().numpy(), k)
     assert np.array_equal(chosen.cpu().numpy(), ri) and np.allclose(weights.cpu().numpy(), rw, rtol=1e-5)
     check(y, *layer.ref(hh, chosen.cpu().numpy(), weights.cpu().numpy(), "bf16"), "bf16")
+
+
+def test_two_graphs_share_a_workspace():
+    """Layers of different sizes captured over one workspace and replayed in turn,
+    with eager calls over it in between."""
+    dev = device()
+    k, layers = 2, [Layer(5, 200, 136), Layer(4, 72, 2056, 128, False, seed=9)]
+    sizes = [(20, 200), (2, 72)]
+    args = []
+    for i, ((T, d), layer) in enumerate(zip(sizes, layers)):
+        x, ids, w = inputs(60 + i, T, k, 4, d, "bf16")
+        args.append((torch.from_numpy(x).to(dev).to(torch.bfloat16), torch.from_numpy(ids).to(dev), torch.from_numpy(w).to(dev)))
+    need = max(rs.lora_w4_moe_workspace_bytes(*layer.stores, torch.bfloat16, a[0].shape[0], k) for layer, a in zip(layers, args))
+    ws = torch.full((need,), 0xA5, dtype=torch.uint8, device=dev)
+    want = [hbits(rs.lora_w4_moe(*layer.stores, *a)) for layer, a in zip(layers, args)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for layer, a in zip(layers, args):
+            rs.lora_w4_moe(*layer.stores, *a, ws=ws)
+    torch.cuda.synchronize()
+    graphs, ys = [], []
+    for layer, a in zip(layers, args):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            ys.append(rs.lora_w4_moe(*layer.stores, *a, ws=ws))
+        graphs.append(g)
+    for turn in range(4):
+        for i in (turn % 2, 1 - turn % 2, turn % 2):
+            ys[i].fill_(7.0)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            assert np.array_equal(hbits(ys[i]), want[i])
+            assert np.array_equal(hbits(rs.lora_w4_moe(*layers[1 - i].stores, *args[1 - i], ws=ws)), want[1 - i])
