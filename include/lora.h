@@ -721,8 +721,8 @@ int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void
  * For more tokens there is lora_w4_apply_experts.
  * Errors: INVALID_ARG (null pointers, T < 0, k < 1, ldx < d_in, ldy < d_out,
  * stores that do not fit together, an unknown act, ws too small); UNSUPPORTED
- * (sizes as lora_w4_bytes, ffn above LORA_W4_MOE_MAX_FFN, T above
- * LORA_W4_MOE_MAX_TOKENS, k above LORA_W4_MOE_MAX_K, unknown dtype, alignment).
+ * (sizes as lora_w4_bytes, ffn as any other, T above LORA_W4_MOE_MAX_TOKENS, k
+ * above LORA_W4_MOE_MAX_K, unknown dtype, alignment).
  *
  * lora_w4_moe_workspace_bytes: bytes of ws (host only; 0 when T is 0, and on
  * invalid arguments).  Scratch: no initialization, and not shared by calls in
@@ -731,7 +731,7 @@ int lora_w4_apply_experts(const lora_w4_store* store_host, int dtype, const void
 enum lora_moe_act { LORA_MOE_SILU = 0, LORA_MOE_GELU_TANH = 1 };
 #define LORA_W4_MOE_MAX_TOKENS 64
 #define LORA_W4_MOE_MAX_K 32
-#define LORA_W4_MOE_MAX_FFN 16384
+#define LORA_W4_MOE_MAX_FFN LORA_W4_MAX_DIM
 size_t lora_w4_moe_workspace_bytes(const lora_w4_store* gate_host, const lora_w4_store* up_host,
                                    const lora_w4_store* down_host, int dtype, int T, int k);
 int lora_w4_moe(const lora_w4_store* gate_host, const lora_w4_store* up_host, const lora_w4_store* down_host, int dtype,

@@ -67,7 +67,7 @@ LORA_MOE_SILU = 0
 LORA_MOE_GELU_TANH = 1
 LORA_W4_MOE_MAX_TOKENS = 64
 LORA_W4_MOE_MAX_K = 32
-LORA_W4_MOE_MAX_FFN = 16384
+LORA_W4_MOE_MAX_FFN = LORA_W4_MAX_DIM
 LORA_W8_MAX_IN = 131064
 LORA_W8_MAX_OUT = 1 << 20
 LORA_W8_MAX_ROWS = 1 << 20

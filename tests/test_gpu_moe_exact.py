@@ -20,6 +20,10 @@ LONG = [
     (40, 2, 2, 24, 16384, 128, False, "bf16", "f32", "silu"),
     (40, 2, 2, 72, 16376, 32, True, "f32", "bf16", "silu"),
     (2, 2, 2, 24, 8200, 64, False, "f32", "f32", "gelu_tanh"),
+    (1, 2, 3, 264, 18944, 128, True, "bf16", "bf16", "silu"),
+    (33, 1, 2, 72, 32776, 64, True, "bf16", "bf16", "gelu_tanh"),
+    (1, 1, 1, 40, 65544, 32, True, "f32", "f32", "silu"),
+    (19, 2, 3, 24, 32776, 128, False, "f32", "f32", "silu"),
 ]
 
 

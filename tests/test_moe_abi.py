@@ -76,6 +76,18 @@ def test_refusals(lib):
     assert lib.lora_last_hip_error() == 0
 
 
+def test_experts_as_wide_as_any_matrix(lib):
+    """h goes through LDS in pieces, as x does: ffn is bounded as every side of
+    a 4-bit matrix is."""
+    for ffn in (16392, 18944, 32776, 1 << 20):
+        g, d = store(d_out=ffn), down(d_in=ffn)
+        for dt, parts in ((BF16, 2), (F32, 3)):
+            need = lib.lora_w4_moe_workspace_bytes(C.byref(g), C.byref(g), C.byref(d), dt, 64, 32)
+            assert need >= 64 * 32 * parts * 2 * ffn, ffn
+        assert lib.lora_w4_moe(C.byref(g), C.byref(g), C.byref(d), BF16, 0, None, 64, None, 64, 0, 2, None, None, None, 0, None) == 0
+    assert lib.lora_last_hip_error() == 0
+
+
 class Held:
     """What the binding's checks read of a store."""
     device_index, d_in, d_out, n = 0, 64, 40, 4
