@@ -102,3 +102,75 @@ def test_activations(case):
     y, bound = act_bounds(layer, x, ids, w, act, dtype)
     off = np.abs(run(layer, group, 32, scales, dtype, x, ids, w, act).double().cpu().numpy() - y)
     assert (off <= bound).all(), f"{float((off / bound).max()):.3g} of the bound"
+
+
+def test_stores_past_31_bits():
+    """The last experts of stores of more than 2^31 bytes of codes are those of
+    the same stores in reverse order."""
+    dev = device()
+    g = torch.Generator(device=dev).manual_seed(11)
+    n, d, ffn, group = 36, 4096, 32768, 128
+
+    def random(d_out, d_in):
+        q = torch.randint(0, 256, (n, d_out, d_in // 2), device=dev, generator=g, dtype=torch.uint8)
+        assert q.numel() > 2 ** 31
+        return q, (torch.rand(n, d_out, d_in // group, device=dev, generator=g) / (4 * d_in ** 0.5)).bfloat16()
+
+    mats = [random(ffn, d), random(ffn, d), random(d, ffn)]
+    stores = [rs.lora_w4_pack(q, s, group=group) for q, s in mats]
+    turned = [rs.lora_w4_pack(q.flip(0), s.flip(0), group=group) for q, s in mats]
+    del mats
+    for T, k, dt in ((1, 3, torch.bfloat16), (50, 1, torch.bfloat16), (2, 2, torch.float32)):
+        note(f"moe past 31 bits {T} {k} {dt}")
+        x = torch.randn(T, d, device=dev, generator=g).to(dt)
+        ids = (n - 1 - torch.arange(T * k, device=dev, dtype=torch.int32) % 7).view(T, k)
+        w = torch.rand(T, k, device=dev, generator=g)
+        y = rs.lora_w4_moe(*stores, x, ids, w)
+        assert torch.isfinite(y).all() and y.float().std() > 0.01
+        assert np.array_equal(hbits(y), hbits(rs.lora_w4_moe(*turned, x, n - 1 - ids, w)))
+
+
+def test_calls_of_several_threads():
+    """Host threads with a stream each, at once, on sizes whose kernels take
+    different amounts of LDS, 8-bit layers among them: the results of calls made
+    alone."""
+    import threading
+
+    dev = device()
+    g = torch.Generator(device=dev).manual_seed(3)
+    jobs = []
+    layer = ExactLayer(8, 4, 4104, 136, 136, 64, True, "bf16")
+    stores = [pack(m.packed(), 64, "bf16", dev) for m in (layer.gate, layer.up, layer.down)]
+    for T in (1, 7, 40):
+        x, ids, w = layer.inputs(T, T, 2)
+        a = [torch.from_numpy(v).to(dev) for v in (x, ids, w)]
+        a[0] = a[0].bfloat16()
+        jobs.append(lambda a=a: rs.lora_w4_moe(*stores, *a))
+    base = rs.lora_w8_pack(torch.randint(-127, 128, (520, 4104), dtype=torch.int8, device=dev, generator=g),
+                           torch.rand(520, device=dev, generator=g))
+    for T in (2, 40, 700):
+        x = torch.randn(T, 4104, device=dev, generator=g).bfloat16()
+        jobs.append(lambda x=x: rs.lora_w8_apply(base, x))
+    got, failed = [None] * len(jobs), []
+    start = threading.Barrier(len(jobs))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            start.wait(60)
+            with torch.cuda.stream(streams[i]):
+                got[i] = [jobs[i]() for _ in range(20)]
+            streams[i].synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for job, ys in zip(jobs, got):
+        want = hbits(job())
+        assert len(ys) == 20 and all(np.array_equal(hbits(y), want) for y in ys)
