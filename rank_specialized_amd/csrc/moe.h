@@ -67,4 +67,41 @@ inline MoePlan moe_plan_call(int n, int ffn, int d_out, int dtype, int T, int k)
   return p;
 }
 
+// A form of a kernel: 16-row tiles of a product; kernel 1: 16-output blocks of a
+// workgroup and waves to a block; kernel 2: blocks of a wave and waves to them
+// (of moe_down_blocks blocks in all); tiles of codes in flight per wave and block.
+struct MoeForm {
+  int tiles, blocks, waves, ahead;
+};
+
+// Kernel 1: two waves share a block's inputs, four blocks to a workgroup.  Two
+// departures where one 16-row tile holds a product:
+// - float32 rows whose workgroups would not reach every compute unit: one block,
+//   four waves.  A unit without work counts (3 tokens, 6 of 8 experts 4096 -> 1368:
+//   kernel 1 20.3 us, and 23.3 with the four blocks).
+// - wide layers of four tokens or more an expert, a group to a tile: a wave to
+//   all inputs of a block, eight blocks, so that half as many workgroups bring
+//   the rows (64 tokens, 8 of 64 experts 2048 -> 1408: kernel 1 40.1 us, and
+//   45.1 otherwise; with one token an expert 57 otherwise, and 69 so; with
+//   groups of 32, whose registers do not suffice, 53 otherwise and 74 so).
+enum { kMoeUpTwo, kMoeUpOne, kMoeUpWide, kMoeUpPlain };
+constexpr MoeForm kMoeUpForms[] = {{2, 2, 4, 2}, {1, 1, 4, 2}, {1, 8, 1, 3}, {1, 4, 2, 2}};
+inline int moe_up_form(const MoePlan& p, int dtype, int sub) {
+  if (p.up_two) return kMoeUpTwo;
+  if (dtype != LORA_DTYPE_BF16) return 2 * p.entries * p.h_tiles < 256 ? kMoeUpOne : kMoeUpPlain;
+  return p.up_wide && sub == 1 ? kMoeUpWide : kMoeUpPlain;
+}
+
+// Kernel 2: four blocks of their own waves, two to a block (one token, 8 of 64
+// experts 1408 -> 2048: 7.4 us, and 8.9 with eight blocks, two to a wave; 7
+// tokens, 4 of 32: 13.3 and 14.9).  Two 16-row tiles: eight blocks, two to a
+// wave (64 tokens, 8 of 64: 36.2 us, and 42.7 with four blocks): half as many
+// workgroups bring the rows.  One workgroup at most to a compute unit, and long
+// inputs: eight waves to two blocks (one token, 2 of 8 experts 14336 -> 4096: 19.9
+// us, and 29.4 with two waves to a block; 2 of 16 10752 -> 6144 17.9, 24.4; 2 of 8
+// 4096 -> 4096 8.8, 9.6; with 6 tiles of inputs, 4 of 32 768 -> 2048, 6.3 and 5.8).
+enum { kMoeDownTwo, kMoeDownDeep, kMoeDownPlain };
+constexpr MoeForm kMoeDownForms[] = {{2, 2, 2, 2}, {1, 2, 8, 2}, {1, 1, 2, 2}};
+inline int moe_down_form(const MoePlan& p) { return p.down_two ? kMoeDownTwo : (p.down_deep ? kMoeDownDeep : kMoeDownPlain); }
+
 }  // namespace lora

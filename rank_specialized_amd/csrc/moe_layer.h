@@ -601,41 +601,34 @@ hipError_t run_down(const MoeCall& c, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Waves to a block of 16 outputs, and blocks to a workgroup.
-// Kernel 1: two waves share a block's inputs, four blocks to a
-// workgroup.  Two departures:
-// - float32 rows whose workgroups would not reach every compute unit: one block,
-//   four waves.  These kernels are bound by the instructions that widen codes,
-//   so a unit without work counts (3 tokens, 6 of 8 experts 4096 -> 1368: kernel
-//   1 20.3 us, and 23.3 with the four blocks).
-// - wide layers of four tokens or more an expert, a group to a tile: a wave to
-//   all inputs of a block, eight blocks, so that half as many workgroups bring
-//   the rows (64 tokens, 8 of 64 experts 2048 -> 1408: kernel 1 40.1 us, and
-//   45.1 otherwise; with one token an expert 57 otherwise, and 69 so; with
-//   groups of 32, whose registers do not suffice, 53 otherwise and 74 so).
+template <typename E, int KIND, int SUB, int F>
+hipError_t run_up_form(const MoeCall& c, hipStream_t stream) {
+  constexpr MoeForm f = kMoeUpForms[F];
+  return run_up<E, KIND, SUB, f.tiles, f.blocks, f.waves, f.ahead>(c, stream);
+}
 template <typename E, int KIND, int SUB>
 hipError_t launch_up(const MoeCall& c, hipStream_t stream) {
-  if (c.plan.up_two) return run_up<E, KIND, SUB, 2, 2, 4, 2>(c, stream);
+  const int form = moe_up_form(c.plan, c.dtype, SUB);
+  if (form == kMoeUpTwo) return run_up_form<E, KIND, SUB, kMoeUpTwo>(c, stream);
   if constexpr (XFrag<E>::kParts > 1) {
-    if (2 * c.plan.entries * c.plan.h_tiles < 256) return run_up<E, KIND, SUB, 1, 1, 4, 2>(c, stream);
+    if (form == kMoeUpOne) return run_up_form<E, KIND, SUB, kMoeUpOne>(c, stream);
   } else if constexpr (SUB == 1) {
-    if (c.plan.up_wide) return run_up<E, KIND, SUB, 1, 8, 1, 3>(c, stream);
+    if (form == kMoeUpWide) return run_up_form<E, KIND, SUB, kMoeUpWide>(c, stream);
   }
-  return run_up<E, KIND, SUB, 1, 4, 2, 2>(c, stream);
+  return run_up_form<E, KIND, SUB, kMoeUpPlain>(c, stream);
 }
-// Kernel 2: four blocks of their own waves, two to a block (one token, 8 of 64
-// experts 1408 -> 2048: 7.4 us, and 8.9 with eight blocks, two to a wave; 7
-// tokens, 4 of 32: 13.3 and 14.9).  Two 16-row tiles: eight blocks, two to a
-// wave (64 tokens, 8 of 64: 36.2 us, and 42.7 with four blocks): half as many
-// workgroups bring the rows.  One workgroup at most to a compute unit, and long
-// inputs: eight waves to two blocks (one token, 2 of 8 experts 14336 -> 4096: 19.9
-// us, and 29.4 with two waves to a block; 2 of 16 10752 -> 6144 17.9, 24.4; 2 of 8
-// 4096 -> 4096 8.8, 9.6; with 6 tiles of inputs, 4 of 32 768 -> 2048, 6.3 and 5.8).
+template <typename E, int KIND, int SUB, int F>
+hipError_t run_down_form(const MoeCall& c, hipStream_t stream) {
+  constexpr MoeForm f = kMoeDownForms[F];
+  return run_down<E, KIND, SUB, f.tiles, f.blocks, f.waves, f.ahead>(c, stream);
+}
 template <typename E, int KIND, int SUB>
 hipError_t launch_down(const MoeCall& c, hipStream_t stream) {
-  if (c.plan.down_two) return run_down<E, KIND, SUB, 2, 2, 2, 2>(c, stream);
-  if (c.plan.down_deep) return run_down<E, KIND, SUB, 1, 2, 8, 2>(c, stream);
-  return run_down<E, KIND, SUB, 1, 1, 2, 2>(c, stream);
+  switch (moe_down_form(c.plan)) {
+    case kMoeDownTwo: return run_down_form<E, KIND, SUB, kMoeDownTwo>(c, stream);
+    case kMoeDownDeep: return run_down_form<E, KIND, SUB, kMoeDownDeep>(c, stream);
+    default: return run_down_form<E, KIND, SUB, kMoeDownPlain>(c, stream);
+  }
 }
 
 template <typename E, bool UP>

@@ -1,17 +1,34 @@
-"""The kernels' forms that calls of the 8-bit products take, by csrc/w8.h itself,
-compiled for the CPU: at the sizes of the GPU tests they are those that
-tests/test_w8_plan.py restates, every one of them among them."""
+"""The kernels' forms that calls of the experts' layer and of the 8-bit products
+take, by csrc/moe.h and csrc/w8.h themselves, compiled for the CPU: at the sizes
+of the GPU tests they are those that tests/test_moe_plan.py and
+tests/test_w8_plan.py restate, every one of them among them."""
 import os
 import shutil
 import subprocess
 
 import pytest
 
+from test_gpu_moe import CASES
+from test_gpu_moe_exact import LONG
 from test_gpu_w8 import SIZES
+from test_moe_plan import kernels
 from test_w8_plan import kernel
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
+MOE = """
+#include <cstdio>
+#include "moe.h"
+using namespace lora;
+int main() {
+  int T, k, n, d, ffn, group, dtype;
+  while (std::scanf("%d %d %d %d %d %d %d", &T, &k, &n, &d, &ffn, &group, &dtype) == 7) {
+    const MoePlan p = moe_plan_call(n, ffn, d, dtype, T, k);
+    const MoeForm u = kMoeUpForms[moe_up_form(p, dtype, w4_sub(group))], v = kMoeDownForms[moe_down_form(p)];
+    std::printf("%d %d %d %d %d %d %d\\n", moe_x_parts(dtype), u.tiles, u.blocks, u.waves, v.tiles, moe_down_blocks(v.tiles == 2), v.waves);
+  }
+}
+"""
 W8 = """
 #include <cstdio>
 #include "w8.h"
@@ -35,6 +52,13 @@ def forms(tmp_path, program, calls):
     lines = "\n".join(" ".join(map(str, c)) for c in calls)
     out = subprocess.run([str(tmp_path / "t")], input=lines, check=True, capture_output=True, text=True, timeout=30).stdout
     return [tuple(map(int, line.split())) for line in out.splitlines()]
+
+
+def test_experts_layer(tmp_path):
+    got = forms(tmp_path, MOE, [(*c[:6], 1 if c[8] == "bf16" else 0) for c in CASES + LONG])
+    assert got == [(*up, *down) for up, down in map(kernels, CASES + LONG)]
+    assert {g[:4] for g in got} == {(1, 1, 4, 2), (1, 1, 8, 1), (1, 2, 2, 4), (3, 1, 1, 4), (3, 1, 4, 2), (3, 2, 2, 4)}
+    assert {(g[0], *g[4:]) for g in got} == {(p, *d) for p in (1, 3) for d in ((1, 4, 2), (1, 4, 8), (2, 8, 2))}
 
 
 def test_8_bit_products(tmp_path):
