@@ -45,10 +45,24 @@ struct W8Plan {
   size_t ws_bytes;
 };
 // Rows and values that a workgroup of the few-rows kernel rounds by itself, at
-// most.  Rounded so, and by a kernel before (us, a call in a graph; on its own,
-// where the host's second launch counts): 5 rows 4096 -> 4096 9.5, 9.7; 9.0, 11.1;
-// 5 rows 3584 -> 3584 8.1, 7.9; 7.7, 11.0; 8 rows 2048 -> 2048 6.4, 6.2; 7.0, 11.0;
-// 12 rows 1280 -> 4096 6.8, 5.9; 6.9, 11.0; 8 rows 512 -> 512 4.2, 5.4; 7.2, 11.1.
+// most: what its registers hold.  Rounded so, and by a kernel before, us a call:
+//                            in a graph     on its own
+//     1 row  3584 ->   512    4.4   6.3     9.0  13.9
+//     1 row  3584 -> 18944   13.1  15.3    13.5  16.5
+//     1 row  4096 -> 65536   45.2  48.5    45.6  49.1
+//     4 rows 5120 -> 18944   20.1  22.4    20.5  22.7
+//     5 rows 3584 ->  3584    7.9   8.1     8.7  13.0
+//     5 rows 4096 ->  4096    9.4   9.9     9.8  13.3  (float32 9.3, 9.8; 10.0, 12.9)
+//     5 rows 4096 -> 32768   25.0  28.2    25.3  28.4
+//     8 rows  512 ->   512    4.2   5.2     8.6  13.2
+//     8 rows 2048 ->  2048    6.2   6.1     8.5  13.2
+//     8 rows 2048 -> 32768   12.9  15.3    13.3  15.9
+//    12 rows 1280 ->  4096    6.4   5.9     8.5  13.3
+//    12 rows 1280 -> 32768   12.1  12.2    12.4  13.3
+//    16 rows 1024 ->  4096    6.2   6.0     8.7  13.2
+//    16 rows 1024 -> 33000   15.1  12.4    15.2  13.4
+// So it is slower in a graph for 12 to 16 short rows, by 0.5 us, and by 2.7 where
+// they meet very many outputs.
 constexpr int kW8FusedRows = 16;
 constexpr int kW8FusedValues = 5 * 8 * 512;  // kHold pieces of 8 per thread (w8_rows.hip)
 

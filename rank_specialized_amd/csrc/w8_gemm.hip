@@ -2,13 +2,14 @@
 //
 //   y[t, o] = s_x[t] s_w[o] sum_k q_x[t, k] q_w[o, k]
 //
-// bounded by the integer matrix cores and, for many rows, by the power that they
-// may take: at 8192 rows 4096 -> 14336 they are busy 85 % of the cycles, and the
-// clock falls to 1.3 to 1.55 GHz (406 us, 2370 TOPS; a large plain product, 8192
-// cubed, reaches 2440).  A workgroup takes 256 rows x 256 outputs, its eight waves
-// 128 x 64 each; or 128 x 128, with two groups of waves over the inputs, where
-// that gives more compute units work (1024 rows 3584 -> 3584 18.8 us, and 38.5
-// with the large ones; the choice is w8_plan_call's).
+// bounded by the integer matrix cores and, for many rows, by the clock that their
+// power leaves: 8192 rows 4096 -> 14336 back to back run at 1.73 to 1.86 GHz, with
+// the matrix cores busy 65 % of the cycles (386 us on one set of inputs, 2490 TOPS;
+// 401 to 418 in turn with others; a large plain product, 8192 cubed, reaches 2440).
+// A workgroup takes 256 rows x 256 outputs, its eight waves 128 x 64 each; or 128 x
+// 128, with two groups of waves over the inputs, where that gives more compute
+// units work (1024 rows 3584 -> 3584 18.8 us, and 38.5 with the large ones; the
+// choice is w8_plan_call's).
 //
 // Both operands go through LDS, 64 inputs at a time, in four stages that loads
 // write directly; the operands of a step are read into registers during the
