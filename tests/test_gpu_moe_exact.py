@@ -174,3 +174,24 @@ def test_calls_of_several_threads():
     for job, ys in zip(jobs, got):
         want = hbits(job())
         assert len(ys) == 20 and all(np.array_equal(hbits(y), want) for y in ys)
+
+
+@pytest.mark.parametrize("T,dtype", [(2, "f32"), (24, "f32"), (64, "f32"), (24, "bf16"), (64, "bf16")])
+def test_values_that_are_no_numbers(T, dtype):
+    """An infinity or a NaN (of any payload) in a row reaches its own row alone, in
+    the forms that tests/test_gpu_moe.py does not take."""
+    dev = device()
+    layer = ExactLayer(9, 16, 264, 4104, 136, 128, True, dtype)
+    x, ids, w = layer.inputs(10, T, 4)
+    stores = [pack(m.packed(), 128, "bf16", dev) for m in (layer.gate, layer.up, layer.down)]
+    a = [torch.from_numpy(v).to(dev) for v in (x, ids, w)]
+    a[0] = a[0].to(DT[dtype])
+    base = hbits(rs.lora_w4_moe(*stores, *a))
+    low = np.array([0x7F800001, 0xFF80FFFF], np.uint32).view(np.float32)  # NaNs whose upper half is an infinity's
+    for bad in [np.inf, -np.inf, np.nan] + (list(low) if dtype == "f32" else []):
+        z = x.copy()
+        z[1, 263] = bad
+        y = rs.lora_w4_moe(*stores, torch.from_numpy(z).to(dev).to(DT[dtype]), *a[1:])
+        assert not torch.isfinite(y[1]).any(), bad
+        keep = np.arange(T) != 1
+        assert np.array_equal(hbits(y)[keep], base[keep]), bad
